@@ -389,6 +389,69 @@ cc3d_status cc3d_forward_noalloc(const cc3d_desc *desc, const void *x, int t,
                                  const void *residual, const void *next_cache_in,
                                  void *next_cache_out, void *stream);
 
+/* ---- Transformer operators ------------------------------------------------
+ *
+ * What the VAE's mid-block (RMS_norm -> 1x1 q, k, v product -> attention per
+ * frame -> 1x1 product + x, "Cosmos3 Wan VAE" §10.6) and a transformer over
+ * streamed latents need around the convs.  They take caller-owned device
+ * memory only (no handle, no workspace), so any number of calls may run at
+ * once on streams that do not share outputs, and every call can be captured
+ * into a graph (make one call of a kind on the device before capturing).
+ * All arguments are checked before anything is launched; conventions and
+ * errors are those above.  Inference only: there are no gradients here. */
+
+/* Activation of cc3d_linear: none, SiLU, GELU (erf), GELU (tanh form). */
+typedef enum {
+  CC3D_ACT_NONE = 0,
+  CC3D_ACT_SILU = 1,
+  CC3D_ACT_GELU = 2,
+  CC3D_ACT_GELU_TANH = 3
+} cc3d_act;
+
+/* Residual addition, RMS norm and an output in 16 or 8 bits, one pass:
+ *   h[r,c] = bf16(x[r,c] + residual[r,c])           (h = x without residual)
+ *   a[r,c] = h[r,c] * sqrt(c) / max(sqrt(sum_c h^2 + c * eps), 1e-12) * gamma[c] (+ beta[c])
+ *   a      = SiLU(a) when silu != 0
+ *   y = bf16(a);   q = E4M3(a / s), saturated to +-448
+ * with s = max_c |a[r,c]| / 448 per row, written to scales[r] (1 for a row of
+ * zeros, at least 1e-36), or s = scale for every row.  eps = 0 gives
+ * rms_norm's definition, eps > 0 the one with the mean square + eps.  The
+ * codes feed cc3d_linear (scales as its x_scales) or, with one scale, a
+ * CC3D_FP8_E4M3 conv plan (scale as its x_scale).
+ *   x, residual, h, y  [rows][c] bf16, 16-byte aligned; residual, h, y
+ *                      nullable; h and y may be x or the residual itself
+ *   q                  [rows][c] bytes, 8-byte aligned, nullable
+ *   gamma, beta        [c] fp32, 16-byte aligned; beta nullable
+ *   scales             [rows] fp32, nullable
+ * c % 8 == 0 and c <= 16384, else CC3D_ERR_UNSUPPORTED.  At least one of h, y,
+ * q; q needs exactly one of scales and scale >= 1e-36 (scale is ignored
+ * without q), else CC3D_ERR_INVALID_ARG.  Any other overlap of an output
+ * with an argument is CC3D_ERR_ALIAS.  rows = 0 does nothing. */
+cc3d_status cc3d_add_rms_norm(const void *x, const void *residual, const float *gamma,
+                              const float *beta, long long rows, int c, float eps, int silu,
+                              void *h, void *y, void *q, float *scales, float scale,
+                              void *stream);
+
+/* Matrix product with its epilogue, fp32 accumulation, rounded once:
+ *   y[m,n] = bf16(act(s_x[m] * s_w[n] * sum_k x[m,k] weight[n,k] + bias[n]) + residual[m,n])
+ * (s_x = s_w = 1 for CC3D_BF16.)
+ *   x       [m] rows of k elements, ldx elements apart; bf16 or E4M3 codes
+ *   weight  [n] rows of k elements, ldw apart (PyTorch's Linear order), x's type
+ *   bias    [n] fp32, nullable
+ *   residual [m] rows of n bf16, ldr apart, nullable; may be y itself (ldr == ldy)
+ *   y       [m] rows of n bf16, ldy apart; elements between rows are not touched
+ *   CC3D_FP8_E4M3: w_scales [n] fp32, and x_scales [m] fp32 or one x_scale > 0
+ *   (the other NULL / 0); CC3D_BF16: all of them NULL / 0.
+ * x, weight, y, residual, bias and w_scales 16-byte aligned.  k, ldx, ldw
+ * multiples of 8 (bf16) or 16 (E4M3); n, ldy, ldr multiples of 8; m, n, k and
+ * row distances at most 2^30, else CC3D_ERR_UNSUPPORTED.  m = 0 does nothing.
+ * One kernel launch; the same arguments give the same bytes on every call. */
+cc3d_status cc3d_linear(const void *x, long long ldx, const void *weight, long long ldw,
+                        const float *bias, const void *residual, long long ldr, void *y,
+                        long long ldy, long long m, int n, int k, cc3d_dtype dtype, cc3d_act act,
+                        const float *x_scales, float x_scale, const float *w_scales,
+                        void *stream);
+
 #ifdef __cplusplus
 }
 #endif

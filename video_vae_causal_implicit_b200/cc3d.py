@@ -20,6 +20,7 @@ LIB_PATH = os.path.join(PKG, "libcc3d.so")
  ERR_TOO_LARGE) = range(9)
 BF16, FP32, FP8_E4M3 = 0, 1, 2
 EPI_BIAS, EPI_BIAS_RESIDUAL, EPI_BIAS_RMS_SILU, EPI_BIAS_RMS = 0, 1, 2, 3
+ACT_NONE, ACT_SILU, ACT_GELU, ACT_GELU_TANH = 0, 1, 2, 3
 VARIANT_NONE, VARIANT_UMMA, VARIANT_THIN, VARIANT_FP32 = 0, 1, 2, 3
 
 _STATUS_NAMES = {0: "CC3D_OK", 1: "CC3D_ERR_INVALID_ARG", 2: "CC3D_ERR_UNSUPPORTED",
@@ -60,7 +61,7 @@ class HostCall(ctypes.Structure):
 
 
 # name -> (restype, argtypes)
-_VP, _I = ctypes.c_void_p, ctypes.c_int
+_VP, _I, _LL, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float
 SIGNATURES = {
     "cc3d_plan_create": (_I, [ctypes.POINTER(Desc), ctypes.POINTER(_VP)]),
     "cc3d_plan_destroy": (_I, [_VP]),
@@ -83,6 +84,9 @@ SIGNATURES = {
     "cc3d_launch_count": (ctypes.c_uint64, []),
     "cc3d_forward_noalloc": (_I, [ctypes.POINTER(Desc), _VP, _I, _VP, _VP, _VP, _VP, _VP, _VP,
                                   _VP]),
+    "cc3d_add_rms_norm": (_I, [_VP, _VP, _VP, _VP, _LL, _I, _F, _I, _VP, _VP, _VP, _VP, _F, _VP]),
+    "cc3d_linear": (_I, [_VP, _LL, _VP, _LL, _VP, _VP, _LL, _VP, _LL, _LL, _I, _I, _I, _I, _VP, _F,
+                         _VP, _VP]),
 }
 
 _lib = None
@@ -337,6 +341,94 @@ def quantize_e4m3(x, scale, q, stream=None):
     check(lib().cc3d_quantize_e4m3(_ptr(x), x.numel(), float(scale), _ptr(q), _stream(stream)),
           "cc3d_quantize_e4m3")
     return q
+
+
+# ---- transformer operators ---------------------------------------------------------
+#
+# The C calls see addresses only, so these wrappers check what the addresses
+# stand for: type, device (the current one), shape and strides.
+
+def _arg(t, name, dtypes, device, shape=None, rows=False):
+    """The address of `t` (None stays None), checked.  rows: the last
+    dimension is contiguous, the one before it may be strided; else the
+    tensor is contiguous."""
+    if t is None:
+        return None
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if rows:
+        if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+            raise ValueError(f"{name}: a matrix with contiguous rows is expected")
+    elif not t.is_contiguous():
+        raise ValueError(f"{name}: not contiguous")
+    return t.data_ptr()
+
+
+def _device(t, name):
+    import torch
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
+    return t.device
+
+
+def _row_step(t):
+    # (the distance of a single row is free: any legal one will do)
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _types():
+    import torch
+    return (torch.bfloat16,), (torch.float32,), (torch.float8_e4m3fn, torch.uint8)
+
+
+def linear(x, weight, y, *, bias=None, residual=None, act=ACT_NONE, x_scales=None, w_scales=None,
+           x_scale=0.0, stream=None):
+    """y = act(x @ weight.T (scaled) + bias) + residual (cc3d_linear).
+
+    x [m, k] and weight [n, k] are bf16, or both E4M3 codes (float8_e4m3fn or
+    uint8) with w_scales [n] and x_scales [m] (or one x_scale); bias fp32 [n];
+    residual and y bf16 [m, n] (y may be the residual).  Rows may be strided."""
+    b16, f32, b8 = _types()
+    dev = _device(x, "x")
+    fp8 = x.dtype in b8
+    ops = b8 if fp8 else b16
+    px = _arg(x, "x", ops, dev, rows=True)
+    m, k = x.shape
+    pw = _arg(weight, "weight", ops, dev, rows=True)
+    n = weight.shape[0]
+    if weight.shape[1] != k:
+        raise ValueError(f"weight: {weight.shape[1]} columns, x has {k}")
+    py = _arg(y, "y", b16, dev, (m, n), rows=True)
+    pr = _arg(residual, "residual", b16, dev, (m, n), rows=True)
+    check(lib().cc3d_linear(
+        px, _row_step(x), pw, _row_step(weight), _arg(bias, "bias", f32, dev, (n,)), pr,
+        _row_step(residual) if residual is not None else 0, py, _row_step(y), m, n, k,
+        FP8_E4M3 if fp8 else BF16, act, _arg(x_scales, "x_scales", f32, dev, (m,)), x_scale,
+        _arg(w_scales, "w_scales", f32, dev, (n,)), _stream(stream)), "cc3d_linear")
+    return y
+
+
+def add_rms_norm(x, gamma, *, residual=None, beta=None, eps=0.0, silu=False, h=None, y=None,
+                 q=None, scales=None, scale=0.0, stream=None):
+    """RMS norm of x (+ residual) over the last dimension, with an output in
+    16 bits (y), in E4M3 (q, with row scales written to `scales` or one given
+    `scale`), and the sum itself (h); see cc3d_add_rms_norm.  Outputs are the
+    tensors given; returns None."""
+    b16, f32, b8 = _types()
+    dev = _device(x, "x")
+    c = x.shape[-1]
+    rows = x.numel() // c if c else 0
+    shape = x.shape
+    check(lib().cc3d_add_rms_norm(
+        _arg(x, "x", b16, dev), _arg(residual, "residual", b16, dev, shape),
+        _arg(gamma, "gamma", f32, dev, (c,)), _arg(beta, "beta", f32, dev, (c,)), rows, c, eps,
+        1 if silu else 0, _arg(h, "h", b16, dev, shape), _arg(y, "y", b16, dev, shape),
+        _arg(q, "q", b8, dev, shape), _arg(scales, "scales", f32, dev, shape[:-1]), scale,
+        _stream(stream)), "cc3d_add_rms_norm")
 
 
 def sync_status(stream=None):

@@ -1,0 +1,703 @@
+// linear.cu -- y = act(x w^T (scaled) + bias) + residual on the tensor cores
+// (cc3d_linear): bf16 or FP8 E4M3 operands, fp32 accumulation in tensor
+// memory, everything after the product in the epilogue.
+//
+//   acc[m][n] = sum_k x[m][k] w[n][k]
+//   y[m][n]   = bf16(act(acc * s_x[m] * s_w[n] + b[n]) + r[m][n])
+//
+// Two kernels:
+//  * linear_kernel, many rows: persistent 128 x NT tiles of y (256 x NT on a
+//    CTA pair), operands by TMA through a ring of 128-byte K chunks, two
+//    accumulators in tensor memory so that a tile's epilogue runs under the
+//    next tile's MMAs.  Bound: tensor pipe (or HBM for short K).
+//  * linear_split_kernel, few rows: bound by the weights' bytes.  The roles
+//    are swapped (the 128 MMA rows are output channels, the columns are the
+//    few tokens), and a cluster of CTAs splits K so that every SM streams
+//    weights; the partial products meet in distributed shared memory, added
+//    in rank order (the result does not depend on scheduling).
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <mutex>
+
+#include "internal.h"
+#include "ops.h"
+#include "ptx.cuh"
+
+namespace cc3d {
+
+namespace {
+
+constexpr uint32_t kRowBytes = 128;  // one K chunk of a row: 64 bf16 or 128 E4M3
+constexpr int kTileRows = 128;       // MMA rows per CTA
+constexpr uint32_t kAStage = kTileRows * kRowBytes;
+constexpr int kEpiWarps = 8;  // two per tensor-memory lane quarter
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr size_t kSmemMost = 227 * 1024;
+constexpr uint64_t kDrainNs = 1000000000ull;
+
+// act() in fp32.  The exponential and the reciprocal are the hardware's
+// (relative error about 2^-21), far below the bf16 rounding of y.
+template <int N>
+__device__ __forceinline__ void activate(float (&v)[N], int act) {
+  if (act == CC3D_ACT_SILU) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] = __fdividef(v[e], 1.f + __expf(-v[e]));
+  } else if (act == CC3D_ACT_GELU_TANH) {
+    // a (1 + tanh u) / 2 = a / (1 + exp(-2 u)), u = sqrt(2 / pi) (a + 0.044715 a^3)
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const float u2 = 1.5957691216057308f * fmaf(0.044715f * v[e] * v[e], v[e], v[e]);
+      v[e] = __fdividef(v[e], 1.f + __expf(-u2));
+    }
+  } else if (act == CC3D_ACT_GELU) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) v[e] = 0.5f * v[e] * erfcf(v[e] * -0.70710678118654752f);
+  }
+}
+
+struct Layout {
+  uint32_t stage, bars, total;  // bytes
+};
+__host__ __device__ inline Layout ring_layout(int b_rows, int stages) {
+  Layout l;
+  l.stage = kAStage + static_cast<uint32_t>(b_rows) * kRowBytes;
+  l.bars = l.stage * static_cast<uint32_t>(stages);
+  l.total = l.bars + 8u * (2u * stages + 5u) + 16u;
+  return l;
+}
+
+// Tiles of a launch, dealt to clusters round robin in groups of kGroup row
+// tiles: the clusters of one wave share few rows of x and few of w in L2.
+struct TileWalk {
+  int m_tiles, n_tiles;
+  static constexpr int kGroup = 8;
+  __device__ __forceinline__ void at(int i, int &mt, int &nt) const {
+    const int per = kGroup * n_tiles;
+    const int g = i / per, r = i - g * per;
+    const int rows = min(kGroup, m_tiles - g * kGroup);
+    nt = r / rows;
+    mt = g * kGroup + (r - nt * rows);
+  }
+};
+
+template <bool FP8, bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_kernel(const __grid_constant__ CUtensorMap map_x,
+                  const __grid_constant__ CUtensorMap map_w, const LinearArgs p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int b_rows = PAIR ? p.nt / 2 : p.nt;  // weight rows this CTA loads
+  const Layout L = ring_layout(b_rows, p.stages);
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + L.bars);
+  uint64_t *empty = full + p.stages;
+  uint64_t *acc_full = empty + p.stages;  // [2]
+  uint64_t *acc_empty = acc_full + 2;     // [2]
+  uint64_t *drain = acc_empty + 2;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+
+  const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
+  const int cid = PAIR ? blockIdx.x / 2 : blockIdx.x;
+  const int ncl = PAIR ? gridDim.x / 2 : gridDim.x;
+  const bool leader = rank == 0;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  constexpr int kChunk = FP8 ? 128 : 64;  // K elements of a chunk
+  const int nk = (p.k + kChunk - 1) / kChunk;
+  constexpr int kRowsPerTile = PAIR ? 2 * kTileRows : kTileRows;
+  const TileWalk walk{(p.m + kRowsPerTile - 1) / kRowsPerTile, (p.n + p.nt - 1) / p.nt};
+  const int n_tiles = walk.m_tiles * walk.n_tiles;
+  const uint32_t tmem_cols = 2u * p.nt;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], PAIR ? 2 * kEpiWarps : kEpiWarps);
+    }
+    mbar_init(drain, 1);
+    fence_mbar_init();
+    prefetch_tmap(&map_x);
+    prefetch_tmap(&map_w);
+  }
+  if (warp == 1) {
+    if constexpr (PAIR) {
+      tmem_alloc_pair(tmem_slot, tmem_cols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, tmem_cols);
+      tmem_relinquish();
+    }
+  }
+  tc_fence_before();
+  if (PAIR)
+    cluster_sync();
+  else
+    __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t smem_base = smem_u32(smem);
+  bool ok = true;
+  griddep_launch_dependents();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // both CTAs' loads complete on the leader's barriers, which the leader
+      // arms for the bytes of both
+      const uint32_t lead_full = PAIR ? mapa_shared(smem_u32(full), 0u) : 0u;
+      const uint32_t tx = (PAIR ? 2u : 1u) * L.stage;
+      int s = 0;
+      uint32_t ph = 0, used = 0, par = 0;
+      griddep_wait();
+      for (int t = cid; t < n_tiles && ok; t += ncl) {
+        int mt, nt;
+        walk.at(t, mt, nt);
+        const int row_x = mt * kRowsPerTile + rank * kTileRows;
+        const int row_w = nt * p.nt + rank * b_rows;
+        for (int kc = 0; kc < nk; ++kc) {
+          if (!mbar_wait_bounded(&empty[s], ph ^ 1, p.wait_limit_ns, p.status, 20)) {
+            ok = false;
+            break;
+          }
+          if (leader) mbar_arrive_expect_tx(&full[s], tx);
+          used |= 1u << s;
+          par = (par & ~(1u << s)) | (ph << s);
+          const uint32_t dst = smem_base + s * L.stage;
+          if constexpr (PAIR) {
+            tma_load_2d_pair(dst, &map_x, lead_full + 8u * s, kc * kChunk, row_x);
+            tma_load_2d_pair(dst + kAStage, &map_w, lead_full + 8u * s, kc * kChunk, row_w);
+          } else {
+            tma_load_2d(dst, &map_x, &full[s], kc * kChunk, row_x);
+            tma_load_2d(dst + kAStage, &map_w, &full[s], kc * kChunk, row_w);
+          }
+          if (++s == p.stages) { s = 0; ph ^= 1; }
+        }
+      }
+      // every load lands before the CTA may exit (the leader's barriers count
+      // both CTAs' loads; the follower waits at the final cluster barrier)
+      if (!leader) used = 0;
+      for (int i = 0; i < p.stages; ++i)
+        if (used >> i & 1u) mbar_wait_bounded(&full[i], par >> i & 1u, kDrainNs, nullptr, 0);
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      const uint32_t idesc = FP8 ? idesc_e4m3_f32(kRowsPerTile, p.nt)
+                                 : idesc_bf16_f32(kRowsPerTile, p.nt);
+      const uint64_t a0 = smem_desc_sw128(smem_base, 1024u);
+      const uint64_t b0 = smem_desc_sw128(smem_base + kAStage, 1024u);
+      int s = 0, it = 0;
+      uint32_t ph = 0;
+      for (int t = cid; t < n_tiles && ok; t += ncl, ++it) {
+        const int buf = it & 1;
+        const uint32_t up = static_cast<uint32_t>((it >> 1) & 1);
+        if (!(PAIR ? mbar_wait_bounded_cluster(&acc_empty[buf], up ^ 1, p.wait_limit_ns, p.status,
+                                               21)
+                   : mbar_wait_bounded(&acc_empty[buf], up ^ 1, p.wait_limit_ns, p.status, 21))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem_base + static_cast<uint32_t>(buf * p.nt);
+        for (int kc = 0; kc < nk; ++kc) {
+          if (!mbar_wait_bounded(&full[s], ph, p.wait_limit_ns, p.status, 22)) {
+            ok = false;
+            break;
+          }
+          const uint64_t a = a0 + ((s * L.stage) >> 4), b = b0 + ((s * L.stage) >> 4);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t acc = (kc | j) != 0;
+            if constexpr (PAIR && FP8) umma_e4m3_pair(d, a + 2 * j, b + 2 * j, idesc, acc);
+            else if constexpr (PAIR) umma_bf16_pair(d, a + 2 * j, b + 2 * j, idesc, acc);
+            else if constexpr (FP8) umma_e4m3(d, a + 2 * j, b + 2 * j, idesc, acc);
+            else umma_bf16(d, a + 2 * j, b + 2 * j, idesc, acc);
+          }
+          if constexpr (PAIR) umma_commit_pair(&empty[s], 3);
+          else umma_commit(&empty[s]);
+          if (++s == p.stages) { s = 0; ph ^= 1; }
+        }
+        if (!ok) break;
+        if constexpr (PAIR) umma_commit_pair(&acc_full[buf], 3);
+        else umma_commit(&acc_full[buf]);
+      }
+      // every MMA is complete before tensor memory is freed
+      if constexpr (PAIR) umma_commit_pair(drain, 1);
+      else umma_commit(drain);
+      mbar_wait_bounded(drain, 0, kDrainNs, nullptr, 0);
+    }
+  } else {
+    const int q = warp % 4;              // tensor-memory lanes this warp may read
+    const int half = (warp - 2) / 4;     // its half of the tile's columns
+    const int cols = p.nt / 2;
+    const uint32_t free_bar = PAIR ? mapa_shared(smem_u32(acc_empty), 0u) : 0u;
+    griddep_wait();
+    int it = 0;
+    for (int t = cid; t < n_tiles; t += ncl, ++it) {
+      int mt, nt;
+      walk.at(t, mt, nt);
+      const int row = mt * kRowsPerTile + rank * kTileRows + q * 32 + lane;
+      const bool live = row < p.m;
+      const int n0 = nt * p.nt + half * cols;
+      const int n1 = min(n0 + cols, p.n);  // (may be <= n0: nothing to store)
+      __nv_bfloat16 *yr = p.y + static_cast<long long>(row) * p.ldy;
+      const __nv_bfloat16 *rr =
+          p.residual ? p.residual + static_cast<long long>(row) * p.ldr : nullptr;
+      // the residual's rows into L2 while the MMAs run
+      if (rr && live && n1 > n0) bulk_prefetch_l2(rr + n0, static_cast<uint32_t>(n1 - n0) * 2u);
+      const float xs = FP8 && live ? (p.x_scales ? p.x_scales[row] : p.x_scale) : 1.f;
+      const int buf = it & 1;
+      const uint32_t up = static_cast<uint32_t>((it >> 1) & 1);
+      uint32_t got = 0;
+      if (lane == 0)
+        got = mbar_wait_bounded(&acc_full[buf], up, p.wait_limit_ns, p.status, 23) ? 1u : 0u;
+      got = __shfl_sync(0xffffffffu, got, 0);
+      if (!got) break;
+      tc_fence_after();
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                             static_cast<uint32_t>(buf * p.nt + half * cols);
+      for (int j = 0; j < cols; j += 32) {
+        __syncwarp();
+        uint32_t raw[32];
+        tmem_ld16_nowait(taddr + j, raw);
+        tmem_ld16_nowait(taddr + j + 16, raw + 16);
+        tmem_wait_ld();
+        tmem_regs_after_wait<32>(raw);
+        if (j + 32 == cols) {
+          // the accumulator is in registers: the next tile's MMAs may start
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (PAIR) mbar_arrive_remote_relaxed(free_bar + 8u * buf);
+            else mbar_arrive(&acc_empty[buf]);
+          }
+        }
+#pragma unroll
+        for (int g = 0; g < 32; g += 8) {
+          const int c = n0 + j + g;
+          if (c >= n1 || !live) continue;
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(raw[g + e]);
+          if constexpr (FP8) {
+            const float4 s0 = *reinterpret_cast<const float4 *>(p.w_scales + c);
+            const float4 s1 = *reinterpret_cast<const float4 *>(p.w_scales + c + 4);
+            const float ws[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= xs * ws[e];
+          }
+          if (p.bias) {
+            const float4 s0 = *reinterpret_cast<const float4 *>(p.bias + c);
+            const float4 s1 = *reinterpret_cast<const float4 *>(p.bias + c + 4);
+            const float bs[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += bs[e];
+          }
+          activate(v, p.act);
+          if (rr) {
+            const uint4 r4 = *reinterpret_cast<const uint4 *>(rr + c);
+            const uint32_t rw[4] = {r4.x, r4.y, r4.z, r4.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              v[e] += __uint_as_float(e & 1 ? rw[e / 2] & 0xffff0000u : rw[e / 2] << 16);
+          }
+          uint4 o;
+          o.x = pack_bf16x2(v[0], v[1]);
+          o.y = pack_bf16x2(v[2], v[3]);
+          o.z = pack_bf16x2(v[4], v[5]);
+          o.w = pack_bf16x2(v[6], v[7]);
+          *reinterpret_cast<uint4 *>(yr + c) = o;
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (PAIR) cluster_sync();  // (the peer may still write or signal into this CTA)
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    if constexpr (PAIR) tmem_dealloc_pair(tmem_base, tmem_cols);
+    else tmem_dealloc(tmem_base, tmem_cols);
+  }
+}
+
+// ---- few rows -----------------------------------------------------------------------
+
+constexpr int kSplitThreads = 192;
+
+__host__ __device__ inline uint32_t split_total(int nt, int stages) {
+  const Layout l = ring_layout(nt, stages);
+  // the ring, later the partial sums [nt][128] fp32 in its place
+  const uint32_t part = static_cast<uint32_t>(nt) * kTileRows * 4u;
+  return (l.bars > part ? l.bars : part) + 8u * (2u * stages + 1u) + 16u;
+}
+
+template <bool FP8>
+__global__ void __launch_bounds__(kSplitThreads)
+    linear_split_kernel(const __grid_constant__ CUtensorMap map_x,
+                        const __grid_constant__ CUtensorMap map_w, const LinearArgs p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const Layout L = ring_layout(p.nt, p.stages);
+  const uint32_t part_bytes = static_cast<uint32_t>(p.nt) * kTileRows * 4u;
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + (L.bars > part_bytes ? L.bars : part_bytes));
+  uint64_t *empty = full + p.stages;
+  uint64_t *acc_full = empty + p.stages;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_full + 1);
+
+  const int split = p.split;
+  const int rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int tile = blockIdx.x / split;
+  const int w_tiles = (p.n + kTileRows - 1) / kTileRows;
+  const int row_w = (tile % w_tiles) * kTileRows;  // output channels of the tile
+  const int row_x = (tile / w_tiles) * p.nt;       // and its tokens
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  constexpr int kChunk = FP8 ? 128 : 64;
+  const int nk = (p.k + kChunk - 1) / kChunk;
+  const int k0 = static_cast<int>(static_cast<long long>(nk) * rank / split);
+  const int k1 = static_cast<int>(static_cast<long long>(nk) * (rank + 1) / split);
+  uint32_t tmem_cols = 32;
+  while (tmem_cols < static_cast<uint32_t>(p.nt)) tmem_cols *= 2;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(acc_full, 1);
+    fence_mbar_init();
+    prefetch_tmap(&map_x);
+    prefetch_tmap(&map_w);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t smem_base = smem_u32(smem);
+  griddep_launch_dependents();
+  griddep_wait();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0, used = 0, par = 0;
+      for (int kc = k0; kc < k1; ++kc) {
+        if (!mbar_wait_bounded(&empty[s], ph ^ 1, p.wait_limit_ns, p.status, 24)) break;
+        mbar_arrive_expect_tx(&full[s], L.stage);
+        used |= 1u << s;
+        par = (par & ~(1u << s)) | (ph << s);
+        const uint32_t dst = smem_base + s * L.stage;
+        tma_load_2d(dst, &map_w, &full[s], kc * kChunk, row_w);
+        tma_load_2d(dst + kAStage, &map_x, &full[s], kc * kChunk, row_x);
+        if (++s == p.stages) { s = 0; ph ^= 1; }
+      }
+      for (int i = 0; i < p.stages; ++i)
+        if (used >> i & 1u) mbar_wait_bounded(&full[i], par >> i & 1u, kDrainNs, nullptr, 0);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc =
+          FP8 ? idesc_e4m3_f32(kTileRows, p.nt) : idesc_bf16_f32(kTileRows, p.nt);
+      const uint64_t a0 = smem_desc_sw128(smem_base, 1024u);
+      const uint64_t b0 = smem_desc_sw128(smem_base + kAStage, 1024u);
+      int s = 0;
+      uint32_t ph = 0;
+      for (int kc = k0; kc < k1; ++kc) {
+        if (!mbar_wait_bounded(&full[s], ph, p.wait_limit_ns, p.status, 25)) break;
+        const uint64_t a = a0 + ((s * L.stage) >> 4), b = b0 + ((s * L.stage) >> 4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t acc = kc > k0 || j > 0;
+          if constexpr (FP8) umma_e4m3(tmem_base, a + 2 * j, b + 2 * j, idesc, acc);
+          else umma_bf16(tmem_base, a + 2 * j, b + 2 * j, idesc, acc);
+        }
+        umma_commit(&empty[s]);
+        if (++s == p.stages) { s = 0; ph ^= 1; }
+      }
+      // (also after a wait that ran out: the MMAs issued so far complete)
+      umma_commit(acc_full);
+    }
+  }
+  // The partial sums, channel-fastest, take the ring's place: every load has
+  // landed and every MMA has read it once acc_full completes.
+  float *part = reinterpret_cast<float *>(smem);
+  if (warp >= 2) {
+    const int q = warp % 4;
+    uint32_t got = 0;
+    if (lane == 0)
+      got = mbar_wait_bounded(acc_full, 0, p.wait_limit_ns + kDrainNs, p.status, 26) ? 1u : 0u;
+    got = __shfl_sync(0xffffffffu, got, 0);
+    tc_fence_after();
+    if (got) {
+      const int used_cols = min(p.nt, p.m - row_x);
+      for (int j = 0; j < used_cols; j += 16) {
+        __syncwarp();
+        uint32_t raw[16];
+        tmem_ld16_nowait(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + j, raw);
+        tmem_wait_ld();
+        tmem_regs_after_wait<16>(raw);
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          part[(j + e) * kTileRows + q * 32 + lane] = __uint_as_float(raw[e]);
+      }
+    }
+    tc_fence_before();
+  }
+  __syncwarp();
+  if (split > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, tmem_cols);
+  }
+  // rank r finishes the tokens r, r + split, ...; a thread two channels
+  const int pair_c = threadIdx.x % 64;
+  const int c = row_w + 2 * pair_c;
+  if (c < p.n) {
+    float ws0 = 1.f, ws1 = 1.f, b0 = 0.f, b1 = 0.f;
+    if constexpr (FP8) {
+      ws0 = p.w_scales[c];
+      ws1 = p.w_scales[c + 1];
+    }
+    if (p.bias) {
+      b0 = p.bias[c];
+      b1 = p.bias[c + 1];
+    }
+    const int tokens = min(p.nt, p.m - row_x);
+    for (int j = rank + split * (threadIdx.x / 64); j < tokens; j += split * (kSplitThreads / 64)) {
+      const uint32_t at = smem_base + static_cast<uint32_t>(j * kTileRows + 2 * pair_c) * 4u;
+      float v[2] = {0.f, 0.f};
+      if (split == 1) {
+        v[0] = part[j * kTileRows + 2 * pair_c];
+        v[1] = part[j * kTileRows + 2 * pair_c + 1];
+      } else {
+        for (int r = 0; r < split; ++r) {
+          const float2 f = ld_cluster_f32x2(mapa_shared(at, static_cast<uint32_t>(r)));
+          v[0] += f.x;
+          v[1] += f.y;
+        }
+      }
+      const long long row = row_x + j;
+      if constexpr (FP8) {
+        const float xs = p.x_scales ? p.x_scales[row] : p.x_scale;
+        v[0] *= xs * ws0;
+        v[1] *= xs * ws1;
+      }
+      v[0] += b0;
+      v[1] += b1;
+      activate(v, p.act);
+      if (p.residual) {
+        const uint32_t rw = *reinterpret_cast<const uint32_t *>(p.residual + row * p.ldr + c);
+        v[0] += __uint_as_float(rw << 16);
+        v[1] += __uint_as_float(rw & 0xffff0000u);
+      }
+      *reinterpret_cast<uint32_t *>(p.y + row * p.ldy + c) = pack_bf16x2(v[0], v[1]);
+    }
+  }
+  if (split > 1) cluster_sync();  // (peers may still read this CTA's partial sums)
+}
+
+// ---- choice of kernel and tile -----------------------------------------------------
+
+struct Choice {
+  bool split_kernel;
+  int pair, nt, stages, split;
+};
+
+// Relative times in cycles of one SM: a chunk costs its MMAs (a 128 x NT x
+// 64 chunk NT * 2 cycles) or its bytes, a tile an epilogue that the next
+// tile's MMAs hide.
+Choice choose(const LinearArgs &a, bool fp8, int sm_count) {
+  const int nk = (a.k + (fp8 ? 127 : 63)) / (fp8 ? 128 : 64);
+  Choice best = {};
+  double best_t = 1e300;
+  // many rows
+  const int shapes[4][2] = {{1, 256}, {1, 128}, {0, 128}, {0, 64}};
+  for (const auto &sh : shapes) {
+    const int pair = sh[0], nt = sh[1], rows = pair ? 256 : 128;
+    const double tiles = static_cast<double>((a.m + rows - 1) / rows) * ((a.n + nt - 1) / nt);
+    const int slots = pair ? sm_count / 2 : sm_count;
+    const double rounds = static_cast<double>(static_cast<long long>((tiles + slots - 1) / slots));
+    const double bytes = kAStage + (pair ? nt / 2 : nt) * static_cast<double>(kRowBytes);
+    const double mma = nt * 2.0, load = bytes / 64.0;
+    const double epi = 64.0 + nt * (a.act ? 14.0 : 8.0);
+    const double per = nk * (mma > load ? mma : load);
+    const double t = 3000.0 + epi + rounds * (per > epi ? per : epi);
+    if (t < best_t) {
+      best_t = t;
+      best = Choice{false, pair, nt, 0, 1};
+    }
+  }
+  // few rows: clusters split K until every SM streams weights
+  if (a.m <= 512) {
+    int nt = 16;
+    while (nt < a.m && nt < 128) nt += 16;
+    const int tiles = ((a.n + 127) / 128) * ((a.m + nt - 1) / nt);
+    for (int split = 1; split <= 8 && split <= nk; ++split) {
+      const double ctas = static_cast<double>(tiles) * split;
+      const double rounds = static_cast<double>(static_cast<long long>((ctas + 2 * sm_count - 1) / (2 * sm_count)));
+      const double share = ctas < sm_count ? 1.0 : 2.0;  // CTAs of one SM
+      const double bytes = kAStage + nt * static_cast<double>(kRowBytes);
+      const double chunks = (nk + split - 1) / split;
+      const double t = 3500.0 + (split > 1 ? 800.0 : 0.0) +
+                       rounds * (1000.0 + share * chunks * (bytes / 32.0 > nt * 2.0 ? bytes / 32.0
+                                                                                   : nt * 2.0) +
+                                 share * nt * 20.0 / split);
+      if (t < best_t) {
+        best_t = t;
+        best = Choice{true, 0, nt, 0, split};
+      }
+    }
+  }
+  if (best.split_kernel) {
+    // two CTAs per SM
+    best.stages = 8;
+    while (best.stages > 2 && split_total(best.nt, best.stages) + 1024 > kSmemMost / 2 - 1024)
+      --best.stages;
+  } else {
+    best.stages = 8;
+    while (ring_layout(best.pair ? best.nt / 2 : best.nt, best.stages).total + 1024 > kSmemMost)
+      --best.stages;
+  }
+  return best;
+}
+
+using LinearKernel = void (*)(const CUtensorMap, const CUtensorMap, const LinearArgs);
+
+// Pairs of CTAs that can be resident at once, per device (grid of the
+// persistent pair kernel).
+int max_pairs(LinearKernel k, size_t smem, int sm_count) {
+  static std::mutex mu;
+  static int known[64][2] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return sm_count / 2;
+  const int which = k == linear_kernel<true, true>;
+  std::lock_guard<std::mutex> lk(mu);
+  if (!known[dev][which]) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void *>(k), &cfg) !=
+            cudaSuccess ||
+        n < 1) {
+      (void)cudaGetLastError();
+      n = sm_count / 2;
+    }
+    known[dev][which] = n;
+  }
+  return known[dev][which];
+}
+
+cudaError_t prepare_kernels() {
+  // per device: the kernels' shared-memory limit
+  static std::mutex mu;
+  static bool done[64] = {false};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lk(mu);
+  if (done[dev]) return cudaSuccess;
+  const LinearKernel ks[6] = {linear_kernel<false, false>, linear_kernel<false, true>,
+                              linear_kernel<true, false>,  linear_kernel<true, true>,
+                              linear_split_kernel<false>,  linear_split_kernel<true>};
+  for (const LinearKernel k : ks) {
+    e = cudaFuncSetAttribute(reinterpret_cast<const void *>(k),
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kSmemMost));
+    if (e != cudaSuccess) return e;
+  }
+  done[dev] = true;
+  return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_linear(LinearArgs a, const void *x, long long ldx, const void *w,
+                          long long ldw, bool fp8, int sm_count, cudaStream_t stream) {
+  cudaError_t e = prepare_kernels();
+  if (e != cudaSuccess) return e;
+  const Choice c = choose(a, fp8, sm_count);
+  a.nt = c.nt;
+  a.stages = c.stages;
+  a.split = c.split;
+  const int esz = fp8 ? 1 : 2;
+  const uint32_t chunk = kRowBytes / esz;
+  const uint32_t x_rows = c.split_kernel ? c.nt : kTileRows;
+  const uint32_t w_rows = c.split_kernel ? kTileRows : (c.pair ? c.nt / 2 : c.nt);
+  CUtensorMap mx, mw;
+  const uint64_t dx[2] = {static_cast<uint64_t>(a.k), static_cast<uint64_t>(a.m)};
+  const uint64_t dw[2] = {static_cast<uint64_t>(a.k), static_cast<uint64_t>(a.n)};
+  const uint64_t sx[1] = {static_cast<uint64_t>(ldx) * esz};
+  const uint64_t sw[1] = {static_cast<uint64_t>(ldw) * esz};
+  const uint32_t bx[2] = {chunk, x_rows}, bw[2] = {chunk, w_rows};
+  if (!encode_sw128_map(&mx, x, esz, 2, dx, sx, bx) || !encode_sw128_map(&mw, w, esz, 2, dw, sw, bw))
+    return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  unsigned na = 0;
+  attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[na].val.programmaticStreamSerializationAllowed = 1;
+  ++na;
+  LinearKernel k;
+  unsigned cluster = 1;
+  if (c.split_kernel) {
+    k = fp8 ? linear_split_kernel<true> : linear_split_kernel<false>;
+    const unsigned tiles = static_cast<unsigned>(((a.n + 127) / 128) * ((a.m + c.nt - 1) / c.nt));
+    cfg.gridDim = dim3(tiles * c.split);
+    cfg.blockDim = dim3(kSplitThreads);
+    cfg.dynamicSmemBytes = split_total(c.nt, c.stages) + 1024;
+    cluster = c.split;
+  } else {
+    const size_t smem = ring_layout(c.pair ? c.nt / 2 : c.nt, c.stages).total + 1024;
+    const int rows = c.pair ? 256 : 128;
+    const long long tiles =
+        static_cast<long long>((a.m + rows - 1) / rows) * ((a.n + c.nt - 1) / c.nt);
+    if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
+    if (c.pair) {
+      k = fp8 ? linear_kernel<true, true> : linear_kernel<false, true>;
+      const long long pairs = max_pairs(k, kSmemMost, sm_count);
+      cfg.gridDim = dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)));
+      cluster = 2;
+    } else {
+      k = fp8 ? linear_kernel<true, false> : linear_kernel<false, false>;
+      cfg.gridDim = dim3(static_cast<unsigned>(tiles < sm_count ? tiles : sm_count));
+    }
+    cfg.blockDim = dim3(kThreads);
+    // (more than half an SM: one CTA per SM, which the tensor memory wants)
+    cfg.dynamicSmemBytes = smem;
+  }
+  if (cluster > 1) {
+    attr[na].id = cudaLaunchAttributeClusterDimension;
+    attr[na].val.clusterDim.x = cluster;
+    attr[na].val.clusterDim.y = attr[na].val.clusterDim.z = 1;
+    ++na;
+  }
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = na;
+  e = cudaLaunchKernelEx(&cfg, k, mx, mw, static_cast<const LinearArgs>(a));
+  count_launch();
+  return e;
+}
+
+}  // namespace cc3d

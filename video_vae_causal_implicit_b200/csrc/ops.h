@@ -1,0 +1,74 @@
+// ops.h -- the transformer operators' launchers and the small host helpers
+// their entry points share (not part of the public interface).
+#pragma once
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "cc3d.h"
+
+namespace cc3d {
+
+inline bool aligned_to(const void *p, unsigned bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & (bytes - 1u)) == 0;
+}
+inline bool ranges_meet(const void *a, size_t na, const void *b, size_t nb) {
+  if (!a || !b || na == 0 || nb == 0) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+inline cc3d_status status_of(cudaError_t e) {
+  return e == cudaSuccess ? CC3D_OK
+         : e == cudaErrorMemoryAllocation ? CC3D_ERR_OOM
+                                          : CC3D_ERR_CUDA;
+}
+
+// Facts of the current device, looked up once per device: its SM count, and
+// whether it is an sm_100 part.
+struct DeviceInfo {
+  int sm_count;
+  bool sm100;
+};
+bool device_info(DeviceInfo *out);
+
+// A tiled tensor map with `rank` dimensions of bf16 (esz 2) or byte (esz 1)
+// elements, the 128-byte swizzle and zero fill out of bounds.  strides: bytes
+// of dimensions 1 .. rank - 1.
+bool encode_sw128_map(CUtensorMap *m, const void *base, int esz, int rank, const uint64_t *dims,
+                      const uint64_t *strides, const uint32_t *box);
+
+struct AddNormArgs {
+  const __nv_bfloat16 *x, *residual;  // [rows][c]; residual nullable
+  const float *gamma, *beta;          // [c]; beta nullable
+  __nv_bfloat16 *h, *y;               // [rows][c], nullable
+  uint8_t *q;                         // [rows][c] E4M3, nullable
+  float *scales;                      // [rows], nullable: one scale per row
+  float q_scale;                      // the given scale where `scales` is null
+  float eps;
+  long long rows;
+  int c, silu;
+};
+// (ordinary loads for everything a call reads: a read-only load may not
+// see what an earlier, overlapped kernel of the stream wrote)
+cudaError_t launch_add_rms_norm(const AddNormArgs &a, int sm_count, cudaStream_t stream);
+
+struct LinearArgs {
+  const float *x_scales, *w_scales;  // FP8: [m] (nullable) and [n]
+  const float *bias;                 // [n], nullable
+  const __nv_bfloat16 *residual;     // [m][ldr], nullable
+  __nv_bfloat16 *y;                  // [m][ldy]
+  long long ldy, ldr;
+  float x_scale;                     // FP8: where x_scales is null
+  int m, n, k, act;
+  int *status;
+  unsigned long long wait_limit_ns;
+  int nt, stages, split;             // set by launch_linear
+};
+// x [m][ldx] and w [n][ldw]: bf16, or E4M3 bytes (fp8).
+cudaError_t launch_linear(LinearArgs a, const void *x, long long ldx, const void *w,
+                          long long ldw, bool fp8, int sm_count, cudaStream_t stream);
+
+}  // namespace cc3d

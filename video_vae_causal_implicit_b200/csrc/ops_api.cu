@@ -1,0 +1,185 @@
+// ops_api.cu -- entry points of the transformer operators (declared in
+// include/cc3d.h): argument checks, tensor maps and launches.  Every check
+// runs on the host before anything is launched.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <climits>
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+
+#include "cc3d.h"
+#include "internal.h"
+#include "ops.h"
+
+namespace cc3d {
+
+bool device_info(DeviceInfo *out) {
+  static std::mutex mu;
+  static DeviceInfo known[64];
+  static bool have[64] = {false};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  std::lock_guard<std::mutex> lk(mu);
+  if (!have[dev]) {
+    int major = 0, minor = 0, sms = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return false;
+    known[dev].sm100 = major == 10 && minor == 0;
+    known[dev].sm_count = sms;
+    have[dev] = true;
+  }
+  *out = known[dev];
+  return true;
+}
+
+bool encode_sw128_map(CUtensorMap *m, const void *base, int esz, int rank, const uint64_t *dims,
+                      const uint64_t *strides, const uint32_t *box) {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }();
+  if (!fn || rank < 2 || rank > 5) return false;
+  cuuint64_t d[5], s[4];
+  cuuint32_t b[5], one[5] = {1, 1, 1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    if (i > 0) s[i - 1] = strides[i - 1];
+  }
+  return fn(m, esz == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+            static_cast<cuuint32_t>(rank), const_cast<void *>(base), d, s, b, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace cc3d
+
+using namespace cc3d;
+
+extern "C" {
+
+cc3d_status cc3d_add_rms_norm(const void *x, const void *residual, const float *gamma,
+                              const float *beta, long long rows, int c, float eps, int silu,
+                              void *h, void *y, void *q, float *scales, float scale,
+                              void *stream) {
+  if (rows < 0 || c < 1 || !(eps >= 0.f) || !std::isfinite(eps)) return CC3D_ERR_INVALID_ARG;
+  if (rows == 0) return CC3D_OK;  // (such a call may come with null tensors)
+  if (!x || !gamma || (!y && !q && !h)) return CC3D_ERR_INVALID_ARG;
+  // 8 bits need exactly one kind of scale
+  if (q ? (scales != nullptr) == (scale > 0.f && std::isfinite(scale)) : scales != nullptr)
+    return CC3D_ERR_INVALID_ARG;
+  if (q && !scales && (!(scale >= 1e-36f) || !std::isfinite(scale))) return CC3D_ERR_INVALID_ARG;
+  if (c % 8 != 0 || c > 16384) return CC3D_ERR_UNSUPPORTED;
+  if (rows > LLONG_MAX / 65536) return CC3D_ERR_INVALID_ARG;
+  if (!aligned_to(x, 16) || !aligned_to(residual, 16) || !aligned_to(h, 16) ||
+      !aligned_to(y, 16) || !aligned_to(q, 8) || !aligned_to(gamma, 16) ||
+      !aligned_to(beta, 16) || !aligned_to(scales, 4))
+    return CC3D_ERR_ALIGNMENT;
+  const size_t vals = static_cast<size_t>(rows) * c, full = vals * 2;
+  const size_t sb = static_cast<size_t>(rows) * 4, pb = static_cast<size_t>(c) * 4;
+  // h may be x or the residual itself (the stream updated in place), and so
+  // may y: an element is read and written by one thread.  Nothing else meets.
+  const void *in[2] = {x, residual};
+  for (const void *i : in) {
+    if ((h != i && ranges_meet(h, full, i, full)) || (y != i && ranges_meet(y, full, i, full)) ||
+        ranges_meet(q, vals, i, full) || ranges_meet(scales, sb, i, full))
+      return CC3D_ERR_ALIAS;
+  }
+  if (ranges_meet(h, full, y, full) || ranges_meet(h, full, q, vals) ||
+      ranges_meet(y, full, q, vals) || ranges_meet(scales, sb, h, full) ||
+      ranges_meet(scales, sb, y, full) || ranges_meet(scales, sb, q, vals))
+    return CC3D_ERR_ALIAS;
+  const float *par[2] = {gamma, beta};
+  for (const float *g : par)
+    if (ranges_meet(g, pb, h, full) || ranges_meet(g, pb, y, full) ||
+        ranges_meet(g, pb, q, vals) || ranges_meet(g, pb, scales, sb))
+      return CC3D_ERR_ALIAS;
+  DeviceInfo dev;
+  if (!device_info(&dev) || !dev.sm100) return CC3D_ERR_UNSUPPORTED;
+  AddNormArgs a;
+  a.x = static_cast<const __nv_bfloat16 *>(x);
+  a.residual = static_cast<const __nv_bfloat16 *>(residual);
+  a.gamma = gamma;
+  a.beta = beta;
+  a.h = static_cast<__nv_bfloat16 *>(h);
+  a.y = static_cast<__nv_bfloat16 *>(y);
+  a.q = static_cast<uint8_t *>(q);
+  a.scales = scales;
+  a.q_scale = scale;
+  a.eps = eps;
+  a.rows = rows;
+  a.c = c;
+  a.silu = silu != 0;
+  return status_of(launch_add_rms_norm(a, dev.sm_count, static_cast<cudaStream_t>(stream)));
+}
+
+cc3d_status cc3d_linear(const void *x, long long ldx, const void *weight, long long ldw,
+                        const float *bias, const void *residual, long long ldr, void *y,
+                        long long ldy, long long m, int n, int k, cc3d_dtype dtype, cc3d_act act,
+                        const float *x_scales, float x_scale, const float *w_scales,
+                        void *stream) {
+  // (a call without rows may come with null tensors)
+  if ((m != 0 && (!x || !weight || !y)) || m < 0 || n < 1 || k < 1 || ldx < k || ldw < k || ldy < n ||
+      (residual && ldr < n) || act < CC3D_ACT_NONE || act > CC3D_ACT_GELU_TANH)
+    return CC3D_ERR_INVALID_ARG;
+  if (dtype != CC3D_BF16 && dtype != CC3D_FP8_E4M3) return CC3D_ERR_UNSUPPORTED;
+  const bool fp8 = dtype == CC3D_FP8_E4M3;
+  const bool one_scale = x_scale > 0.f && std::isfinite(x_scale);
+  if (fp8 ? (!w_scales || (x_scales != nullptr) == one_scale)
+          : (w_scales || x_scales || x_scale != 0.f))
+    return CC3D_ERR_INVALID_ARG;
+  const int step = fp8 ? 16 : 8;  // operand elements of 16 bytes
+  constexpr long long kMost = 1ll << 30;
+  if (k % step != 0 || ldx % step != 0 || ldw % step != 0 || n % 8 != 0 || ldy % 8 != 0 ||
+      (residual && ldr % 8 != 0) || m > kMost || n > kMost || k > kMost || ldx > kMost ||
+      ldw > kMost || ldy > kMost || (residual && ldr > kMost))
+    return CC3D_ERR_UNSUPPORTED;
+  if (!aligned_to(x, 16) || !aligned_to(weight, 16) || !aligned_to(y, 16) ||
+      !aligned_to(residual, 16) || !aligned_to(bias, 16) || !aligned_to(w_scales, 16) ||
+      !aligned_to(x_scales, 4))
+    return CC3D_ERR_ALIGNMENT;
+  if (m == 0) return CC3D_OK;
+  const size_t esz = fp8 ? 1 : 2, rows = static_cast<size_t>(m), nn = static_cast<size_t>(n);
+  const size_t xb = ((rows - 1) * ldx + k) * esz, wb = ((nn - 1) * ldw + k) * esz;
+  const size_t yb = ((rows - 1) * ldy + nn) * 2, rb = residual ? ((rows - 1) * ldr + nn) * 2 : 0;
+  // y may be the residual itself (the stream updated in place)
+  const bool in_place = residual == y && ldr == ldy;
+  if (ranges_meet(y, yb, x, xb) || ranges_meet(y, yb, weight, wb) ||
+      ranges_meet(y, yb, bias, nn * 4) || ranges_meet(y, yb, w_scales, nn * 4) ||
+      ranges_meet(y, yb, x_scales, rows * 4) || (!in_place && ranges_meet(y, yb, residual, rb)))
+    return CC3D_ERR_ALIAS;
+  DeviceInfo dev;
+  if (!device_info(&dev) || !dev.sm100) return CC3D_ERR_UNSUPPORTED;
+  LinearArgs a = {};
+  a.x_scales = x_scales;
+  a.w_scales = w_scales;
+  a.bias = bias;
+  a.residual = static_cast<const __nv_bfloat16 *>(residual);
+  a.y = static_cast<__nv_bfloat16 *>(y);
+  a.ldy = ldy;
+  a.ldr = ldr;
+  a.x_scale = x_scale;
+  a.m = static_cast<int>(m);
+  a.n = n;
+  a.k = k;
+  a.act = act;
+  a.status = device_status_word();
+  if (!a.status) return CC3D_ERR_CUDA;
+  a.wait_limit_ns = wait_limit_ns();
+  return status_of(launch_linear(a, x, ldx, weight, ldw, fp8, dev.sm_count,
+                                 static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
