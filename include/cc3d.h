@@ -452,6 +452,72 @@ cc3d_status cc3d_linear(const void *x, long long ldx, const void *weight, long l
                         const float *x_scales, float x_scale, const float *w_scales,
                         void *stream);
 
+/* Attention in a sliding window of frames, with sink frames (bf16, fp32
+ * softmax).  A frame is `frame` consecutive tokens.  A query of frame i sees
+ * the keys of frame j when j <= i and (window == 0 or i - j < window or
+ * j < sinks):
+ *   o = sum_j softmax_j(scale * q . k_j) v_j   over the keys it sees;
+ * a query that sees none gives zeros.  frame = 1 is the token-wise sliding
+ * window; window = 1 with sinks = 0 is the mid-block's attention within each
+ * frame ("Cosmos3 Wan VAE" §10.6, WanAttentionBlock).
+ *
+ * A sequence has `total` frames, the chunk of the call included; the chunk's
+ * t frames are its last.  (total < t: the chunk's first frames lie before the
+ * sequence and see nothing.)  With k_frames and q_frames (device, [n],
+ * nullable) sequence b has k_frames[b] frames, of which the last q_frames[b]
+ * <= t are the chunk's, in its first q_frames[b] frames of q and o; rows of o
+ * behind them are left as they were.  Larger or negative values count as the
+ * nearest allowed one.
+ *
+ * k and v are caches that hold the chunk already (cc3d_kv_append writes it):
+ * `slots` frames per sequence.  ring == 0: slot s holds frame s.  ring > 0
+ * (slots == sinks + ring): slots below `sinks` hold the first frames, frame
+ * p >= sinks is in slot sinks + (p - sinks) % ring; the ring has to hold what
+ * the chunk sees, window - 1 + t <= ring.  Slots that no query sees may hold
+ * anything, NaN included.
+ *
+ * q and o [n][t * frame][heads][d], k and v [n][slots * frame][kv_heads][d],
+ * each with its own strides in elements (multiples of 8; the last dimension
+ * is contiguous, so slices of a fused q, k, v product can be passed as they
+ * are).  heads is a multiple of kv_heads; query head h reads kv head
+ * h / (heads / kv_heads).  scale 0 stands for 1 / sqrt(d).
+ *
+ * One kernel launch, no workspace; the same arguments give the same bytes on
+ * every call.  d % 8 == 0, d <= 384, heads / kv_heads <= 128, at most 2^31 -
+ * 1024 tokens in q or in a cache, n and kv_heads <= 65535, else
+ * CC3D_ERR_UNSUPPORTED.  o must not
+ * overlap an input's extent, nor its own rows (CC3D_ERR_ALIAS).  n = 0 and
+ * t = 0 do nothing. */
+typedef struct {
+  int n, heads, kv_heads, d;
+  int frame, t, slots, window, sinks, ring;
+  int total;   /* ignored with k_frames */
+  float scale;
+  const int *q_frames, *k_frames;
+  const void *q, *k, *v;
+  void *o;
+  long long q_seq, q_tok, q_head, k_seq, k_tok, k_head;
+  long long v_seq, v_tok, v_head, o_seq, o_tok, o_head;
+} cc3d_attn_call;
+cc3d_status cc3d_attention(const cc3d_attn_call *call, void *stream);
+
+/* The cache update that goes before cc3d_attention: the chunk's keys and
+ * values ([n][t * frame][kv_heads][d] bf16) into the slots of its frames
+ * (frames and slots as above; frames that the ring has no room for, the
+ * chunk being longer, and frames past the last slot are not written).  The
+ * two caches must not overlap the inputs (CC3D_ERR_ALIAS); they may be
+ * interleaved with each other. */
+typedef struct {
+  int n, kv_heads, d, frame, t, slots, sinks, ring;
+  int total;   /* ignored with k_frames */
+  const int *q_frames, *k_frames;
+  const void *k, *v;
+  void *k_cache, *v_cache;
+  long long k_seq, k_tok, k_head, v_seq, v_tok, v_head;
+  long long kc_seq, kc_tok, kc_head, vc_seq, vc_tok, vc_head;
+} cc3d_kv_call;
+cc3d_status cc3d_kv_append(const cc3d_kv_call *call, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,402 @@
+"""cc3d_attention and cc3d_kv_append on the GPU against the definition in 64
+bits.
+
+Tolerance, from the arithmetic.  A score is a sum of d exact products in fp32
+(off by (d + 8) 2^-23 of the sum of their magnitudes) and enters the exponent
+with two roundings of its own size (2^-23 |s|) beside the hardware
+exponential's 2^-21; a weight is rounded to bf16 (2^-8) before the second
+product while the weights' sum takes it unrounded; that product sums K terms
+in fp32.  With A = sum p |v| / sum p an output is off by at most
+A (2^-8 + 4 e + (K + 8) 2^-22), e the largest score error, and by its own
+rounding, 2^-8 |o|.
+
+That does not show one key too many or too few among thousands, so the masks
+are tested apart, with equal scores (q = 0: every weight is exactly 1) and
+values that are 1 at one token per channel: an output is then 1 / (keys seen)
+if the query sees that token (exact but for the division and the rounding),
+and exactly 0 if not."""
+import math
+
+import pytest
+import torch
+
+from video_vae_causal_implicit_b200 import cc3d
+
+pytestmark = pytest.mark.gpu
+
+
+def slot_of(p, sinks, ring):
+    return p if not ring or p < sinks else sinks + (p - sinks) % ring
+
+
+class Case:
+    """Logical sequences (every frame's k and v) and the caches made of them."""
+
+    def __init__(self, *, n=1, frame=1, t=1, total=1, heads=1, kv=1, d=64, window=0, sinks=0,
+                 ring=0, slots=None, k_frames=None, q_frames=None, seed=0, fill=float("nan")):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        self.n, self.f, self.t, self.heads, self.kv, self.d = n, frame, t, heads, kv, d
+        self.window, self.sinks, self.ring = window, sinks, ring
+        self.all = list(k_frames) if k_frames is not None else [total] * n
+        self.chunk = list(q_frames) if q_frames is not None else [t] * n
+        self.total = total
+        self.dev_all = None if k_frames is None else torch.tensor(k_frames, device="cuda",
+                                                                  dtype=torch.int32)
+        self.dev_chunk = None if q_frames is None else torch.tensor(q_frames, device="cuda",
+                                                                    dtype=torch.int32)
+        most = max(max(self.all), 1)
+        self.slots = slots or (sinks + ring if ring else most)
+        rnd = lambda *s: torch.randn(*s, device="cuda", generator=g).to(torch.bfloat16)  # noqa: E731
+        self.q = rnd(n, t * frame, heads, d)
+        self.lk, self.lv = rnd(n, most * frame, kv, d), rnd(n, most * frame, kv, d)
+        self.fill = fill
+
+    def caches(self):
+        """The caches as the frames before the chunk and the chunk itself leave them."""
+        f = self.f
+        shape = (self.n, self.slots * f, self.kv, self.d)
+        k, v = (torch.full(shape, self.fill, device="cuda", dtype=torch.bfloat16)
+                for _ in range(2))
+        for b in range(self.n):
+            for p in range(self.all[b]):
+                s = slot_of(p, self.sinks, self.ring)
+                if s < self.slots:
+                    k[b, s * f:(s + 1) * f] = self.lk[b, p * f:(p + 1) * f]
+                    v[b, s * f:(s + 1) * f] = self.lv[b, p * f:(p + 1) * f]
+        return k, v
+
+    def args(self):
+        return dict(frame=self.f, window=self.window, sinks=self.sinks, ring=self.ring,
+                    total=self.total, k_frames=self.dev_all, q_frames=self.dev_chunk)
+
+    def run(self, q=None, k=None, v=None, o=None, **kw):
+        if k is None:
+            k, v = self.caches()
+        q = self.q if q is None else q
+        if o is None:
+            o = torch.full(q.shape, 7.0, device="cuda", dtype=torch.bfloat16)
+        cc3d.attention(q, k, v, o, **self.args(), **kw)
+        cc3d.sync_status()
+        return o
+
+    def seen(self, b):
+        """[chunk tokens, all tokens] which keys each query sees."""
+        a, c, f = self.all[b], self.chunk[b], self.f
+        pq = a - c + torch.arange(c * f, device="cuda") // f
+        pk = torch.arange(a * f, device="cuda") // f
+        far = pq[:, None] - pk
+        near = far < self.window if self.window else torch.ones_like(far, dtype=torch.bool)
+        return (far >= 0) & (near | (pk < self.sinks))
+
+    def reference(self, b, scale=None):
+        """(o, tolerance) of sequence b's chunk, in 64 bits: [tokens, heads, d]."""
+        a, c, f, d = self.all[b], self.chunk[b], self.f, self.d
+        seen, g = self.seen(b), self.heads // self.kv
+        scale = scale or d ** -0.5
+        o = torch.zeros(c * f, self.heads, d, device="cuda", dtype=torch.float64)
+        tol = torch.zeros_like(o)
+        for h in range(self.heads if a and c else 0):
+            q = self.q[b, :c * f, h].double()
+            k, v = self.lk[b, :a * f, h // g].double(), self.lv[b, :a * f, h // g].double()
+            s = q @ k.t() * scale
+            mag = (q.abs() @ k.abs().t()) * scale
+            hid = ~seen
+            s = s.masked_fill(hid, -math.inf)
+            p = torch.exp(s - s.amax(1, keepdim=True).clamp_min(-1e300))
+            p = p.masked_fill(hid, 0)
+            l = p.sum(1, keepdim=True)
+            p = torch.where(l > 0, p / l.clamp_min(1e-300), p)
+            o[:, h] = p @ v
+            big = p @ v.abs()
+            err = ((d + 8) * 2.0 ** -23 * mag + 2.0 ** -22 * mag + 2.0 ** -21).masked_fill(hid, 0)
+            e = err.amax(1, keepdim=True)
+            tol[:, h] = (big * (2.0 ** -8 + 4 * e + (a * f + 8) * 2.0 ** -22) +
+                         2.0 ** -8 * o[:, h].abs()) * 1.01 + 1e-30
+        return o, tol
+
+    def check(self, o, scale=None):
+        for b in range(self.n):
+            c = self.chunk[b] * self.f
+            ref, tol = self.reference(b, scale)
+            got = o[b, :c].double()
+            bad = ~((got - ref).abs() <= tol)
+            assert not bad.any(), (b, int(bad.sum()), bad.nonzero()[:3].tolist(),
+                                   float((got - ref).abs().nan_to_num(9e9).max()))
+            assert (o[b, c:] == 7).all(), "rows behind the chunk"
+
+
+CASES = {
+    # one token, growing lengths, head sizes, shared heads
+    "one key": dict(total=1, d=64),
+    "short": dict(total=37, d=8, heads=2, kv=2),
+    "token": dict(total=300, d=128, heads=8, kv=2, n=3),
+    "token mha": dict(total=515, d=80, heads=4, kv=4),
+    "token mqa": dict(total=1000, d=96, heads=32, kv=1),
+    "token wide group": dict(total=130, d=64, heads=128, kv=1),
+    "token odd group": dict(total=700, d=64, heads=6, kv=2),
+    "token long": dict(total=9000, d=128, heads=4, kv=1),
+    "token wide head": dict(total=260, d=384, heads=2, kv=1),
+    # a whole sequence
+    "prefill": dict(t=257, total=257, d=64, heads=3, kv=3),
+    "prefill window": dict(t=700, total=700, d=128, heads=4, kv=2, window=100, sinks=3),
+    "prefill many": dict(t=1500, total=1500, d=128, heads=48, kv=16, window=333, sinks=5),
+    "prefill after past": dict(t=300, total=811, d=72, heads=16, kv=16, window=200, sinks=130),
+    "prefill two": dict(n=2, t=640, total=700, d=96, heads=64, kv=32, window=64),
+    # frames
+    "frames": dict(frame=70, t=3, total=3, d=384, window=1),
+    "frames 200": dict(frame=130, t=2, total=4, d=200, window=2, sinks=1, heads=2, kv=2),
+    "frame of one tile": dict(frame=128, t=2, total=5, d=128, window=2, sinks=1, heads=2, kv=1),
+    "frame large": dict(frame=1560, t=1, total=2, d=384, window=1),
+    "frames many": dict(frame=200, t=4, total=6, d=64, heads=20, kv=20, window=3, sinks=1),
+    # rings, not full, full, wrapped
+    "ring young": dict(total=5, d=64, window=20, sinks=4, ring=20),
+    "ring": dict(total=1003, d=64, window=250, sinks=4, ring=256, heads=2, kv=1),
+    "ring exact": dict(total=777, d=128, window=100, sinks=0, ring=100),
+    "ring chunk": dict(t=40, total=533, d=64, window=200, sinks=7, ring=239, heads=4, kv=2),
+    "ring frames": dict(frame=100, t=2, total=11, d=128, window=3, sinks=1, ring=4, heads=3, kv=3),
+    "ring frames many": dict(frame=330, t=1, total=20, d=64, window=4, sinks=1, ring=4, heads=40,
+                             kv=40),
+    # lengths per sequence, padded chunks, sequences without frames
+    "ragged": dict(n=4, t=1, d=64, heads=4, kv=2, window=50, sinks=2, ring=60,
+                   k_frames=[1, 3, 61, 400]),
+    "padded": dict(n=3, t=50, d=64, heads=2, kv=2, window=30, sinks=1, k_frames=[50, 77, 10],
+                   q_frames=[50, 20, 0]),
+    "empty sequence": dict(n=3, t=2, d=64, heads=2, kv=2, k_frames=[0, 5, 2], q_frames=[0, 2, 2]),
+    "before the start": dict(n=2, t=6, d=64, k_frames=[3, 0], window=4, q_frames=[6, 6]),
+}
+
+
+@pytest.mark.parametrize("name", CASES)
+def test_against_the_definition(name):
+    c = Case(**CASES[name], seed=len(name))
+    # (the reference's chunk of a sequence shorter than it starts before frame 0)
+    if name == "before the start":
+        o = c.run()
+        assert (o[0, :3] == 0).all() and (o[1] == 0).all()
+        short = Case(**dict(CASES[name], q_frames=[3, 0]), seed=len(name))
+        short.q = c.q[:, 3:]
+        short.q = torch.cat([short.q, short.q], 1)
+        ref, tol = short.reference(0)
+        assert ((o[0, 3:].double() - ref).abs() <= tol).all()
+        return
+    c.check(c.run())
+
+
+MASKS = {
+    "tokens": dict(t=400, total=400, d=128, heads=2, kv=2, window=0),
+    "tokens window": dict(t=500, total=500, d=128, heads=2, kv=1, window=129, sinks=2),
+    "tokens window 1": dict(t=300, total=300, d=64, heads=1, kv=1, window=1, sinks=0),
+    "tokens many": dict(t=900, total=1000, d=64, heads=40, kv=20, window=128, sinks=128),
+    "one token": dict(t=1, total=2100, d=128, heads=8, kv=8, window=2000, sinks=8),
+    "ring": dict(t=1, total=3333, d=128, heads=4, kv=1, window=1000, sinks=8, ring=1003),
+    "ring chunk": dict(t=90, total=1234, d=128, heads=2, kv=2, window=311, sinks=3, ring=400),
+    "frames": dict(frame=77, t=4, total=4, d=384, window=2, sinks=1),
+    "frames ring": dict(frame=129, t=2, total=13, d=64, heads=20, kv=20, window=3, sinks=2, ring=4),
+}
+
+
+@pytest.mark.parametrize("name", MASKS)
+def test_masks_key_by_key(name):
+    for seed in range(3):
+        c = Case(**MASKS[name], seed=seed)
+        c.q.zero_()
+        c.lk.normal_(generator=torch.Generator(device="cuda").manual_seed(seed))
+        g = torch.Generator(device="cuda").manual_seed(100 + seed)
+        most = max(c.all) * c.f
+        # marked tokens: anywhere, and at the edges of what some queries see
+        edges = torch.tensor([0, c.f - 1, c.f, c.sinks * c.f - 1, c.sinks * c.f, most - 1,
+                              most - c.f, (max(c.all) - c.window) * c.f,
+                              (max(c.all) - c.window) * c.f - 1], device="cuda").clamp(0, most - 1)
+        at = torch.randint(0, most, (c.d,), device="cuda", generator=g)
+        at[:len(edges)] = edges[:c.d]
+        c.lv.zero_()
+        c.lv[:, at, :, torch.arange(c.d, device="cuda")] = 1
+        o = c.run()
+        for b in range(c.n):
+            seen = c.seen(b)
+            keys = seen.sum(1).double()
+            want = seen[:, at].double() / keys[:, None].clamp_min(1)
+            got = o[b, :c.chunk[b] * c.f].double()
+            for h in range(c.heads):
+                diff = (got[:, h] - want).abs() > want * 2.0 ** -8 * 1.001
+                assert not diff.any(), (name, seed, h, diff.nonzero()[:4].tolist())
+
+
+@pytest.mark.parametrize("name", ["token", "prefill window", "frames", "ring chunk"])
+def test_slices_of_a_fused_product(name):
+    """q, k and v as slices of one buffer, o with gaps, a given scale."""
+    kw = dict(CASES[name], ring=0, slots=None, k_frames=None)
+    kw["t"] = kw["total"]  # the chunk is the whole sequence
+    c = Case(**kw, seed=3)
+    hq, hk, tok = c.heads * c.d, c.kv * c.d, c.t * c.f
+    fused = torch.empty(c.n, tok, hq + 2 * hk + 8, device="cuda", dtype=torch.bfloat16)
+    q = fused[..., :hq].view(c.n, tok, c.heads, c.d)
+    k = fused[..., hq:hq + hk].view(c.n, tok, c.kv, c.d)
+    v = fused[..., hq + hk:hq + 2 * hk].view(c.n, tok, c.kv, c.d)
+    q.copy_(c.q)
+    k.copy_(c.lk)
+    v.copy_(c.lv)
+    wide = torch.full((c.n, tok, c.heads, c.d + 16), 5.0, device="cuda", dtype=torch.bfloat16)
+    o = wide[..., :c.d]
+    c.run(q, k, v, o, scale=0.21)
+    c.check(o, 0.21)
+    assert (wide[..., c.d:] == 5).all()
+    # heads before tokens
+    qt, kt, vt = (x.transpose(1, 2).contiguous().transpose(1, 2) for x in (q, k, v))
+    o2 = c.run(qt, kt, vt, scale=0.21)
+    assert torch.equal(o2, o)
+
+
+def test_large_scores_and_growing_maxima():
+    """Scores that grow along the keys, so that the running maximum moves."""
+    for t, d in ((1, 64), (300, 128), (200, 384)):
+        c = Case(t=t, total=1000, d=d, heads=2, kv=2, seed=4)
+        ramp = torch.linspace(0.1, 12, 1000, device="cuda").view(1, 1000, 1, 1)
+        c.lk = (c.lk.float() * ramp).to(torch.bfloat16)
+        c.check(c.run())
+        c.lk = c.lk.flip(1)
+        c.check(c.run())
+
+
+def test_infinite_key_and_nan_value_are_as_in_the_definition():
+    c = Case(t=1, total=200, d=64, heads=1, kv=1, window=50, seed=2)
+    clean = c.run()
+    # outside the window: no influence, whatever stands there
+    c.lk[0, 100] = float("inf")
+    c.lv[0, 120] = float("nan")
+    assert torch.equal(c.run(), clean)
+    c.lv[0, 180, 0, 5] = float("nan")
+    o = c.run()
+    assert torch.isnan(o[0, 0, 0, 5]) and torch.isfinite(o[0, 0, 0, :5].float()).all()
+
+
+@pytest.mark.parametrize("name", ["token", "prefill window", "ring chunk", "frame large",
+                                  "ring frames many"])
+def test_same_bytes_on_every_call_stream_and_replay(name):
+    c = Case(**CASES[name], seed=1)
+    k, v = c.caches()
+    first = c.run(k=k, v=v)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    outs = []
+    for i in range(9):
+        o = torch.full_like(first, 7)
+        streams[i % 3].wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(streams[i % 3]):
+            cc3d.attention(c.q, k, v, o, **c.args())
+        outs.append(o)
+    torch.cuda.synchronize()
+    o = torch.full_like(first, 7)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cc3d.attention(c.q, k, v, o, **c.args())
+    graph.replay()
+    graph.replay()
+    cc3d.sync_status()
+    for x in outs + [o]:
+        assert torch.equal(x, first)
+
+
+APPEND = {
+    "plain": dict(t=3, total=10, d=64, heads=2, kv=2),
+    "ring": dict(t=2, total=47, d=128, heads=2, kv=2, window=9, sinks=2, ring=10),
+    "into sinks": dict(t=4, total=5, d=64, heads=1, kv=1, window=3, sinks=3, ring=6),
+    "chunk longer than the ring": dict(t=30, total=60, d=64, window=1, sinks=2, ring=7),
+    "frames": dict(frame=50, t=2, total=9, d=96, heads=3, kv=3, window=2, sinks=1, ring=3),
+    "ragged": dict(n=4, t=2, d=64, window=4, sinks=1, ring=5, k_frames=[2, 0, 9, 33],
+                   q_frames=[2, 0, 1, 2]),
+}
+
+
+@pytest.mark.parametrize("name", APPEND)
+def test_append(name):
+    c = Case(**APPEND[name], fill=3.0)
+    want_k, want_v = c.caches()
+    # the caches before the chunk: the frames up to it (later ones of the
+    # chunk's slots still hold what was there)
+    before = Case(**dict(APPEND[name]), fill=3.0)
+    before.lk, before.lv = c.lk, c.lv
+    before.all = [a - q for a, q in zip(c.all, c.chunk)]
+    k, v = before.caches()
+    f = c.f
+    shape = (c.n, c.t * f, 2, c.kv, c.d)
+    new = torch.full(shape, float("nan"), device="cuda", dtype=torch.bfloat16)
+    for b in range(c.n):
+        a, q = c.all[b] * f, c.chunk[b] * f
+        new[b, :q, 0], new[b, :q, 1] = c.lk[b, a - q:a], c.lv[b, a - q:a]
+    args = c.args()
+    args.pop("window")
+    cc3d.kv_append(new[:, :, 0], new[:, :, 1], k, v, **args)
+    cc3d.sync_status()
+    assert torch.equal(k, want_k) and torch.equal(v, want_v)
+
+
+def test_streaming_token_by_token_equals_the_whole_sequence():
+    """Append and attend, one frame a call, over a ring, against one call over
+    the whole sequence; the calls of a step captured once and replayed."""
+    n, frame, steps, heads, kv, d, window, sinks = 2, 24, 12, 4, 2, 64, 3, 1
+    g = torch.Generator(device="cuda").manual_seed(0)
+    rnd = lambda h: torch.randn(n, steps * frame, h, d, device="cuda", generator=g).to(  # noqa: E731
+        torch.bfloat16)
+    q, k, v = rnd(heads), rnd(kv), rnd(kv)
+    whole = torch.empty_like(q)
+    cc3d.attention(q, k, v, whole, frame=frame, window=window, sinks=sinks, total=steps)
+    ring = window
+    kc = torch.full((n, (sinks + ring) * frame, kv, d), float("nan"), device="cuda",
+                    dtype=torch.bfloat16)
+    vc = kc.clone()
+    qs, ks, vs = (x[:, :frame].clone() for x in (q, k, v))
+    o = torch.empty_like(qs)
+    count = torch.zeros(n, device="cuda", dtype=torch.int32)
+
+    def step():
+        cc3d.kv_append(ks, vs, kc, vc, frame=frame, sinks=sinks, ring=ring, k_frames=count)
+        cc3d.attention(qs, kc, vc, o, frame=frame, window=window, sinks=sinks, ring=ring,
+                       k_frames=count)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    kc.fill_(float("nan"))
+    vc.fill_(float("nan"))
+    for i in range(steps):
+        for dst, src in ((qs, q), (ks, k), (vs, v)):
+            dst.copy_(src[:, i * frame:(i + 1) * frame])
+        count.fill_(i + 1)
+        graph.replay()
+        a, b = o.double(), whole[:, i * frame:(i + 1) * frame].double()
+        # the same sums in another order: bf16 steps of the weights and outputs
+        assert ((a - b).abs() <= 2.0 ** -6 * (1 + b.abs())).all()
+    cc3d.sync_status()
+
+
+def test_long_cache_offsets_past_32_bits():
+    """A cache of more than 2^31 elements: 20 sequences, 1 million tokens each,
+    of which the last is read."""
+    n, slots, kv, d = 9, 1 << 20, 2, 128
+    assert n * slots * kv * d > 1 << 31
+    k = torch.zeros(n, slots, kv, d, device="cuda", dtype=torch.bfloat16)
+    v = torch.zeros_like(k)
+    c = Case(n=n, t=1, total=600, d=d, heads=4, kv=kv, window=500, sinks=2, seed=7)
+    q = c.q
+    # the last 498 tokens of a sequence of `slots`, and the two sinks
+    keep = torch.cat([torch.arange(2), torch.arange(slots - 500, slots)]).cuda()
+    k[:, keep], v[:, keep] = c.lk[:, 98:], c.lv[:, 98:]
+    o = torch.empty_like(q)
+    cc3d.attention(q, k, v, o, window=500, sinks=2, total=slots)
+    small = torch.empty_like(q)
+    cc3d.attention(q, c.lk[:, 98:].contiguous(), c.lv[:, 98:].contiguous(), small, total=502)
+    cc3d.sync_status()
+    assert ((o.double() - small.double()).abs() <= 2.0 ** -6 * (1 + small.double().abs())).all()
+    assert o[n - 1].abs().max() > 0
+
+
+def test_no_sequences_and_no_chunk():
+    c = Case(total=4, t=1, d=64)
+    k, v = c.caches()
+    before = cc3d.cc3d_launch_count()
+    cc3d.attention(c.q[:0], k[:0], v[:0], c.q[:0].clone(), total=4)
+    cc3d.attention(c.q[:, :0], k, v, c.q[:, :0].clone(), total=4)
+    cc3d.kv_append(c.q[:, :0], c.q[:, :0], k, v, total=4)
+    assert cc3d.cc3d_launch_count() == before

@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libcc3d.so")
@@ -87,6 +88,8 @@ SIGNATURES = {
     "cc3d_add_rms_norm": (_I, [_VP, _VP, _VP, _VP, _LL, _I, _F, _I, _VP, _VP, _VP, _VP, _F, _VP]),
     "cc3d_linear": (_I, [_VP, _LL, _VP, _LL, _VP, _VP, _LL, _VP, _LL, _LL, _I, _I, _I, _I, _VP, _F,
                          _VP, _VP]),
+    "cc3d_attention": (_I, [_VP, _VP]),
+    "cc3d_kv_append": (_I, [_VP, _VP]),
 }
 
 _lib = None
@@ -429,6 +432,82 @@ def add_rms_norm(x, gamma, *, residual=None, beta=None, eps=0.0, silu=False, h=N
         1 if silu else 0, _arg(h, "h", b16, dev, shape), _arg(y, "y", b16, dev, shape),
         _arg(q, "q", b8, dev, shape), _arg(scales, "scales", f32, dev, shape[:-1]), scale,
         _stream(stream)), "cc3d_add_rms_norm")
+
+
+# cc3d_attn_call and cc3d_kv_call as the C compiler lays them out
+_ATTN_CALL = struct.Struct("@11if6P12q")
+_KV_CALL = struct.Struct("@9i6P12q")
+
+
+def _heads(t, name, b16, dev, frames_of=None):
+    """The address of a [n, tokens, heads, d] bf16 tensor with a contiguous
+    last dimension, checked."""
+    if t.dtype not in b16:
+        raise TypeError(f"{name}: {t.dtype}, expected torch.bfloat16")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.dim() != 4 or (t.shape[3] > 1 and t.stride(3) != 1):
+        raise ValueError(f"{name}: [n, tokens, heads, d] with a contiguous last dimension expected")
+    if frames_of is not None and t.shape[1] % frames_of:
+        raise ValueError(f"{name}: {t.shape[1]} tokens are not whole frames of {frames_of}")
+    return t.data_ptr()
+
+
+def _lengths(n, frame, sinks, ring, total, q_frames, k_frames, dev):
+    import torch
+    if frame < 1:
+        raise ValueError(f"frame: {frame}")
+    i32 = (torch.int32,)
+    if k_frames is None and total is None:
+        raise ValueError("total or k_frames is needed")
+    return (_arg(q_frames, "q_frames", i32, dev, (n,)) or 0,
+            _arg(k_frames, "k_frames", i32, dev, (n,)) or 0, 0 if total is None else total)
+
+
+def attention(q, k, v, o, *, frame=1, window=0, sinks=0, ring=0, total=None, q_frames=None,
+              k_frames=None, scale=0.0, stream=None):
+    """Attention in a sliding window of frames with sink frames
+    (cc3d_attention): q and o [n, t * frame, heads, d], k and v caches
+    [n, slots * frame, kv_heads, d], bf16, any strides with a contiguous last
+    dimension.  total: frames of every sequence, this chunk included, or
+    k_frames (int32 [n], device) one count each; window 0: unlimited."""
+    b16, _, _ = _types()
+    dev = _device(q, "q")
+    n, qt, heads, d = q.shape if q.dim() == 4 else (0, 0, 0, 0)
+    pq_, pk_, total = _lengths(n, frame, sinks, ring, total, q_frames, k_frames, dev)
+    pq, pk = _heads(q, "q", b16, dev, frame), _heads(k, "k", b16, dev, frame)
+    pv, po = _heads(v, "v", b16, dev, frame), _heads(o, "o", b16, dev, frame)
+    kv = k.shape
+    if kv[0] != n or kv[3] != d or v.shape != kv or o.shape != q.shape:
+        raise ValueError(f"q {tuple(q.shape)}, k {tuple(kv)}, v {tuple(v.shape)}, "
+                         f"o {tuple(o.shape)} do not fit")
+    call = _ATTN_CALL.pack(n, heads, kv[2], d, frame, qt // frame, kv[1] // frame, window, sinks,
+                           ring, total, scale, pq_, pk_, pq, pk, pv, po, *q.stride()[:3],
+                           *k.stride()[:3], *v.stride()[:3], *o.stride()[:3])
+    check(lib().cc3d_attention(call, _stream(stream)), "cc3d_attention")
+    return o
+
+
+def kv_append(k, v, k_cache, v_cache, *, frame=1, sinks=0, ring=0, total=None, q_frames=None,
+              k_frames=None, stream=None):
+    """A chunk's keys and values [n, t * frame, kv_heads, d] into the caches
+    [n, slots * frame, kv_heads, d] (cc3d_kv_append); frame counts as in
+    attention, the chunk included."""
+    b16, _, _ = _types()
+    dev = _device(k, "k")
+    n, kt, heads, d = k.shape if k.dim() == 4 else (0, 0, 0, 0)
+    pq_, pk_, total = _lengths(n, frame, sinks, ring, total, q_frames, k_frames, dev)
+    pk, pv = _heads(k, "k", b16, dev, frame), _heads(v, "v", b16, dev, frame)
+    pkc = _heads(k_cache, "k_cache", b16, dev, frame)
+    pvc = _heads(v_cache, "v_cache", b16, dev, frame)
+    cs = k_cache.shape
+    if v.shape != k.shape or v_cache.shape != cs or cs[0] != n or tuple(cs[2:]) != (heads, d):
+        raise ValueError(f"k {tuple(k.shape)}, v {tuple(v.shape)}, k_cache {tuple(cs)}, "
+                         f"v_cache {tuple(v_cache.shape)} do not fit")
+    call = _KV_CALL.pack(n, heads, d, frame, kt // frame, cs[1] // frame, sinks, ring, total, pq_,
+                         pk_, pk, pv, pkc, pvc, *k.stride()[:3], *v.stride()[:3],
+                         *k_cache.stride()[:3], *v_cache.stride()[:3])
+    check(lib().cc3d_kv_append(call, _stream(stream)), "cc3d_kv_append")
 
 
 def sync_status(stream=None):

@@ -71,4 +71,35 @@ struct LinearArgs {
 cudaError_t launch_linear(LinearArgs a, const void *x, long long ldx, const void *w,
                           long long ldw, bool fp8, int sm_count, cudaStream_t stream);
 
+// Which frame of a sequence a cache slot holds: slot s < sinks frame s; the
+// later slots frame s (ring 0), or cyclically the last `ring` frames.
+struct CacheShape {
+  int n, kv_heads, d, frame, slots, sinks, ring;
+  int t;                           // frames of the call's chunk
+  int total;                       // frames of every sequence, the chunk included, ...
+  const int *q_frames, *k_frames;  // ... or per sequence: chunk frames, all frames (nullable)
+};
+
+struct AttnArgs {
+  CacheShape c;
+  int heads, window;       // window: frames, 0 = unlimited
+  float scale_log2;        // softmax scale * log2(e)
+  __nv_bfloat16 *o;
+  long long o_seq, o_tok, o_head;
+  int *status;
+  unsigned long long wait_limit_ns;
+  int group, tok_tile;     // query heads per kv head; tokens per 128 rows
+  int chunks, stages, split, q_tiles;  // set by launch_attention
+};
+struct Strides {
+  long long seq, tok, head;  // in elements
+};
+cudaError_t launch_attention(AttnArgs a, const void *q, const Strides &sq, const void *k,
+                             const Strides &sk, const void *v, const Strides &sv, int sm_count,
+                             cudaStream_t stream);
+cudaError_t launch_kv_append(const CacheShape &c, const __nv_bfloat16 *k, const Strides &sk,
+                             const __nv_bfloat16 *v, const Strides &sv, __nv_bfloat16 *kc,
+                             const Strides &skc, __nv_bfloat16 *vc, const Strides &svc,
+                             int sm_count, cudaStream_t stream);
+
 }  // namespace cc3d

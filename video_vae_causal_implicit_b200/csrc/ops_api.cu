@@ -64,6 +64,64 @@ bool encode_sw128_map(CUtensorMap *m, const void *base, int esz, int rank, const
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+namespace {
+
+// Elements from the first to the last of a [n][tok][head][d] view, plus one.
+long long span(int n, long long toks, int heads, int d, const Strides &s) {
+  return (n - 1) * s.seq + (toks - 1) * s.tok + (heads - 1) * s.head + d;
+}
+
+// Strides that 16-byte pieces and a tensor map allow (only of dimensions with
+// more than one entry; the others are not used).
+bool strides_ok(int n, long long toks, int heads, const Strides &s) {
+  const long long ext[3] = {n, toks, heads}, st[3] = {s.seq, s.tok, s.head};
+  for (int i = 0; i < 3; ++i)
+    if (ext[i] > 1 && (st[i] < 8 || st[i] % 8 != 0 || st[i] > (1ll << 38))) return false;
+  return true;
+}
+
+// Whether no two entries of the view share an element: ordered by stride,
+// each dimension steps over all of the smaller ones.
+bool disjoint_entries(int n, long long toks, int heads, int d, const Strides &s) {
+  long long ext[3] = {n, toks, heads}, st[3] = {s.seq, s.tok, s.head};
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2 - i; ++j)
+      if (st[j] > st[j + 1]) {
+        long long t = st[j];
+        st[j] = st[j + 1];
+        st[j + 1] = t;
+        t = ext[j];
+        ext[j] = ext[j + 1];
+        ext[j + 1] = t;
+      }
+  long long covered = d;
+  for (int i = 0; i < 3; ++i) {
+    if (ext[i] == 1) continue;
+    if (st[i] < covered) return false;
+    covered = (ext[i] - 1) * st[i] + covered;
+  }
+  return true;
+}
+
+constexpr long long kMostTokens = (1ll << 31) - 1024;
+
+// The checks that the cache's shape needs, shared by both calls.
+cc3d_status check_cache(int n, int kv_heads, int d, int frame, int t, int slots, int sinks,
+                        int ring, int total, const int *q_frames, const int *k_frames) {
+  if (n < 0 || kv_heads < 1 || d < 1 || frame < 1 || t < 0 || slots < 1 || sinks < 0 || ring < 0)
+    return CC3D_ERR_INVALID_ARG;
+  if (ring > 0 && static_cast<long long>(sinks) + ring != slots) return CC3D_ERR_INVALID_ARG;
+  if (!k_frames && (total < 0 || (ring == 0 && total > slots))) return CC3D_ERR_INVALID_ARG;
+  if (d % 8 != 0 || d > 384 || n > 65535 || kv_heads > 65535) return CC3D_ERR_UNSUPPORTED;
+  if (static_cast<long long>(slots) * frame > kMostTokens ||
+      static_cast<long long>(t) * frame > kMostTokens)
+    return CC3D_ERR_UNSUPPORTED;
+  if (!aligned_to(q_frames, 4) || !aligned_to(k_frames, 4)) return CC3D_ERR_ALIGNMENT;
+  return CC3D_OK;
+}
+
+}  // namespace
+
 }  // namespace cc3d
 
 using namespace cc3d;
@@ -180,6 +238,99 @@ cc3d_status cc3d_linear(const void *x, long long ldx, const void *weight, long l
   a.wait_limit_ns = wait_limit_ns();
   return status_of(launch_linear(a, x, ldx, weight, ldw, fp8, dev.sm_count,
                                  static_cast<cudaStream_t>(stream)));
+}
+
+cc3d_status cc3d_attention(const cc3d_attn_call *p, void *stream) {
+  if (!p) return CC3D_ERR_INVALID_ARG;
+  const cc3d_status s = check_cache(p->n, p->kv_heads, p->d, p->frame, p->t, p->slots, p->sinks,
+                                    p->ring, p->total, p->q_frames, p->k_frames);
+  if (s != CC3D_OK) return s;
+  if (p->heads < 1 || p->heads % p->kv_heads != 0 || p->window < 0 || !(p->scale >= 0.f) ||
+      !std::isfinite(p->scale))
+    return CC3D_ERR_INVALID_ARG;
+  // a ring has to hold every frame that a query of the chunk sees
+  if (p->ring > 0 && (p->window == 0 || static_cast<long long>(p->window) - 1 + p->t > p->ring))
+    return CC3D_ERR_INVALID_ARG;
+  if (p->heads / p->kv_heads > 128) return CC3D_ERR_UNSUPPORTED;
+  if (p->n == 0 || p->t == 0) return CC3D_OK;  // (such a call may come with null tensors)
+  if (!p->q || !p->k || !p->v || !p->o) return CC3D_ERR_INVALID_ARG;
+  const long long qt = static_cast<long long>(p->t) * p->frame;
+  const long long kt = static_cast<long long>(p->slots) * p->frame;
+  const Strides sq{p->q_seq, p->q_tok, p->q_head}, sk{p->k_seq, p->k_tok, p->k_head},
+      sv{p->v_seq, p->v_tok, p->v_head}, so{p->o_seq, p->o_tok, p->o_head};
+  if (!strides_ok(p->n, qt, p->heads, sq) || !strides_ok(p->n, kt, p->kv_heads, sk) ||
+      !strides_ok(p->n, kt, p->kv_heads, sv) || !strides_ok(p->n, qt, p->heads, so))
+    return CC3D_ERR_UNSUPPORTED;
+  if (!aligned_to(p->q, 16) || !aligned_to(p->k, 16) || !aligned_to(p->v, 16) ||
+      !aligned_to(p->o, 16))
+    return CC3D_ERR_ALIGNMENT;
+  if (!disjoint_entries(p->n, qt, p->heads, p->d, so)) return CC3D_ERR_ALIAS;
+  const size_t ob = static_cast<size_t>(span(p->n, qt, p->heads, p->d, so)) * 2;
+  if (ranges_meet(p->o, ob, p->q, static_cast<size_t>(span(p->n, qt, p->heads, p->d, sq)) * 2) ||
+      ranges_meet(p->o, ob, p->k, static_cast<size_t>(span(p->n, kt, p->kv_heads, p->d, sk)) * 2) ||
+      ranges_meet(p->o, ob, p->v, static_cast<size_t>(span(p->n, kt, p->kv_heads, p->d, sv)) * 2) ||
+      ranges_meet(p->o, ob, p->q_frames, static_cast<size_t>(p->n) * 4) ||
+      ranges_meet(p->o, ob, p->k_frames, static_cast<size_t>(p->n) * 4))
+    return CC3D_ERR_ALIAS;
+  DeviceInfo dev;
+  if (!device_info(&dev) || !dev.sm100) return CC3D_ERR_UNSUPPORTED;
+  AttnArgs a = {};
+  a.c = CacheShape{p->n, p->kv_heads, p->d, p->frame, p->slots, p->sinks, p->ring, p->t, p->total,
+                   p->q_frames, p->k_frames};
+  a.heads = p->heads;
+  a.window = p->window;
+  const float scale = p->scale > 0.f ? p->scale : 1.f / sqrtf(static_cast<float>(p->d));
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.o = static_cast<__nv_bfloat16 *>(p->o);
+  a.o_seq = p->o_seq;
+  a.o_tok = p->o_tok;
+  a.o_head = p->o_head;
+  a.status = device_status_word();
+  if (!a.status) return CC3D_ERR_CUDA;
+  a.wait_limit_ns = wait_limit_ns();
+  return status_of(launch_attention(a, p->q, sq, p->k, sk, p->v, sv, dev.sm_count,
+                                    static_cast<cudaStream_t>(stream)));
+}
+
+cc3d_status cc3d_kv_append(const cc3d_kv_call *p, void *stream) {
+  if (!p) return CC3D_ERR_INVALID_ARG;
+  const cc3d_status s = check_cache(p->n, p->kv_heads, p->d, p->frame, p->t, p->slots, p->sinks,
+                                    p->ring, p->total, p->q_frames, p->k_frames);
+  if (s != CC3D_OK) return s;
+  if (p->n == 0 || p->t == 0) return CC3D_OK;
+  if (!p->k || !p->v || !p->k_cache || !p->v_cache) return CC3D_ERR_INVALID_ARG;
+  const long long nt = static_cast<long long>(p->t) * p->frame;
+  const long long ct = static_cast<long long>(p->slots) * p->frame;
+  const Strides sk{p->k_seq, p->k_tok, p->k_head}, sv{p->v_seq, p->v_tok, p->v_head},
+      skc{p->kc_seq, p->kc_tok, p->kc_head}, svc{p->vc_seq, p->vc_tok, p->vc_head};
+  if (!strides_ok(p->n, nt, p->kv_heads, sk) || !strides_ok(p->n, nt, p->kv_heads, sv) ||
+      !strides_ok(p->n, ct, p->kv_heads, skc) || !strides_ok(p->n, ct, p->kv_heads, svc))
+    return CC3D_ERR_UNSUPPORTED;
+  if (!aligned_to(p->k, 16) || !aligned_to(p->v, 16) || !aligned_to(p->k_cache, 16) ||
+      !aligned_to(p->v_cache, 16))
+    return CC3D_ERR_ALIGNMENT;
+  if (!disjoint_entries(p->n, ct, p->kv_heads, p->d, skc) ||
+      !disjoint_entries(p->n, ct, p->kv_heads, p->d, svc) || p->k_cache == p->v_cache)
+    return CC3D_ERR_ALIAS;
+  void *const out[2] = {p->k_cache, p->v_cache};
+  const size_t ob[2] = {static_cast<size_t>(span(p->n, ct, p->kv_heads, p->d, skc)) * 2,
+                        static_cast<size_t>(span(p->n, ct, p->kv_heads, p->d, svc)) * 2};
+  for (int i = 0; i < 2; ++i)
+    if (ranges_meet(out[i], ob[i], p->k,
+                    static_cast<size_t>(span(p->n, nt, p->kv_heads, p->d, sk)) * 2) ||
+        ranges_meet(out[i], ob[i], p->v,
+                    static_cast<size_t>(span(p->n, nt, p->kv_heads, p->d, sv)) * 2) ||
+        ranges_meet(out[i], ob[i], p->q_frames, static_cast<size_t>(p->n) * 4) ||
+        ranges_meet(out[i], ob[i], p->k_frames, static_cast<size_t>(p->n) * 4))
+      return CC3D_ERR_ALIAS;
+  DeviceInfo dev;
+  if (!device_info(&dev) || !dev.sm100) return CC3D_ERR_UNSUPPORTED;
+  const CacheShape c{p->n, p->kv_heads, p->d, p->frame, p->slots, p->sinks, p->ring, p->t,
+                     p->total, p->q_frames, p->k_frames};
+  return status_of(launch_kv_append(
+      c, static_cast<const __nv_bfloat16 *>(p->k), sk, static_cast<const __nv_bfloat16 *>(p->v), sv,
+      static_cast<__nv_bfloat16 *>(p->k_cache), skc, static_cast<__nv_bfloat16 *>(p->v_cache), svc,
+      dev.sm_count, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"
