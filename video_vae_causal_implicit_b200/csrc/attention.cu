@@ -53,6 +53,16 @@ struct Ranges {
   __device__ __forceinline__ bool has(int s) const {
     return (s >= lo[0] && s < hi[0]) || (s >= lo[1] && s < hi[1]) || (s >= lo[2] && s < hi[2]);
   }
+  // bit i: whether token s + i is in them (i < 32)
+  __device__ __forceinline__ uint32_t bits(int s) const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) m |= below(hi[i] - s) & ~below(lo[i] - s);
+    return m;
+  }
+  static __device__ __forceinline__ uint32_t below(int n) {  // bits 0 .. n - 1
+    return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+  }
   // whether [a, b) lies inside one of them
   __device__ __forceinline__ bool covers(int a, int b) const {
     return (a >= lo[0] && b <= hi[0]) || (a >= lo[1] && b <= hi[1]) || (a >= lo[2] && b <= hi[2]);
@@ -158,8 +168,16 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+// Warps 0 - 3: loads, products, two idle ones (the registers of a warpgroup
+// can be moved only together); then four warps per row tile.
+constexpr int kFirstRowWarp = 4;
+constexpr __host__ __device__ int attn_threads(int nq) { return 32 * kFirstRowWarp + 128 * nq; }
+// 168 registers a thread at launch with 384 threads; the row warps' tile of
+// scores wants more: 136 * 128 + 184 * 256 = 168 * 384.
+constexpr int kRegsFew = 136, kRegsMany = 184;
+
 template <int NQ, int KT>
-__global__ void __launch_bounds__(64 + 128 * NQ, 1)
+__global__ void __launch_bounds__(attn_threads(NQ), 1)
     attn_kernel(const __grid_constant__ CUtensorMap map_q,
                 const __grid_constant__ CUtensorMap map_k,
                 const __grid_constant__ CUtensorMap map_v, const AttnArgs p) {
@@ -245,9 +263,15 @@ __global__ void __launch_bounds__(64 + 128 * NQ, 1)
   griddep_launch_dependents();
   bool ok = true;
 
+  if constexpr (NQ == 2) {
+    if (warp < kFirstRowWarp)
+      regs_fewer<kRegsFew>();
+    else
+      regs_more<kRegsMany>();
+  }
   if (warp == 0) {
     // ------------------------------ loads ---------------------------------------
-    if (lane == 0 && nj > 0) {
+    if (nj > 0 && elect_one()) {
       const int rows = p.tok_tile * p.group;
       mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(NQ * chunks * rows) * 128u);
       for (int q = 0; q < NQ; ++q)
@@ -258,6 +282,7 @@ __global__ void __launch_bounds__(64 + 128 * NQ, 1)
       uint32_t ph = 0, used = 0, par = 0;
       auto load = [&](const CUtensorMap *map, int j) {
         const int tok = tiles.at(j0 + j) * KT;
+#pragma unroll 1
         for (int c = 0; c < chunks && ok; ++c) {
           if (!mbar_wait_bounded(&empty[s], ph ^ 1, p.wait_limit_ns, p.status, 30)) {
             ok = false;
@@ -283,7 +308,7 @@ __global__ void __launch_bounds__(64 + 128 * NQ, 1)
     }
   } else if (warp == 1) {
     // ------------------------------ products ------------------------------------
-    if (lane == 0 && nj > 0) {
+    if (nj > 0 && elect_one()) {
       const uint32_t idesc_s = idesc_bf16_f32(kRows, KT);
       // O in steps of two chunks where they pair up in the ring
       const int wide = (chunks % 2 == 0 && stages % 2 == 0) ? 2 : 1;
@@ -299,6 +324,7 @@ __global__ void __launch_bounds__(64 + 128 * NQ, 1)
       auto fail = [&]() { ok = false; };
       // S[slot] = Q[q] K^T of the key tile at ring position (ks, kp)
       auto qk = [&](int q, int slot, int ks, uint32_t kp, bool wait, bool release) {
+#pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
           if (wait && !mbar_wait_bounded(&full[ks], kp, p.wait_limit_ns, p.status, 31))
             return fail();
@@ -314,6 +340,7 @@ __global__ void __launch_bounds__(64 + 128 * NQ, 1)
       };
       // O[q] (+)= P[slot] V of the value tile at ring position (vs, vp)
       auto pv = [&](int q, int slot, int vs, uint32_t vp, bool wait, bool release, bool first) {
+#pragma unroll 1
         for (int c = 0; c < chunks; c += wide) {
           int v2 = vs;
           uint32_t p2 = vp;
@@ -343,7 +370,11 @@ __global__ void __launch_bounds__(64 + 128 * NQ, 1)
         tc_fence_after();
       };
       auto advance = [&]() {
-        for (int c = 0; c < chunks; ++c) step(s, ph);
+        s += chunks;
+        while (s >= stages) {
+          s -= stages;
+          ph ^= 1;
+        }
       };
       if (!mbar_wait_bounded(q_full, 0, p.wait_limit_ns, p.status, 34)) ok = false;
       if constexpr (NQ == 1) {
@@ -391,9 +422,9 @@ __global__ void __launch_bounds__(64 + 128 * NQ, 1)
       umma_commit(drain);
       mbar_wait_bounded(drain, 0, kDrainNs, nullptr, 0);
     }
-  } else {
+  } else if (warp >= kFirstRowWarp) {
     // ------------------------------ softmax, output ------------------------------
-    const int wg = (warp - 2) / 4;  // this warp's row tile
+    const int wg = (warp - kFirstRowWarp) / 4;  // this warp's row tile
     const int quarter = warp % 4;   // the tensor-memory lanes it may read
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const int r = quarter * 32 + lane;  // its row of the tile
@@ -410,30 +441,42 @@ __global__ void __launch_bounds__(64 + 128 * NQ, 1)
     for (int j = 0; j < nj; ++j) {
       const int slot = NQ == 2 ? wg : (j & 1);
       const uint32_t par = static_cast<uint32_t>(NQ == 2 ? j : (j >> 1)) & 1u;
-      uint32_t got = 0;
-      if (lane == 0)
-        got = mbar_wait_bounded(&s_full[slot], par, p.wait_limit_ns, p.status, 35) ? 1u : 0u;
-      got = __shfl_sync(0xffffffffu, got, 0);
-      if (!got) {
+      if (!mbar_wait_bounded(&s_full[slot], par, p.wait_limit_ns, p.status, 35)) {
         ok = false;
         break;
       }
+      __syncwarp();
       tc_fence_after();
-      uint32_t raw[KT];
-#pragma unroll
-      for (int i = 0; i < KT; i += 16) tmem_ld16_nowait(s_col[slot] + lanes + i, raw + i);
-      tmem_wait_ld();
-      tmem_regs_after_wait<KT>(raw);
       const int t0 = tiles.at(j0 + j) * KT;
       const bool masked = !every.covers(t0, t0 + KT);
-      if (masked) {
+      // The row's scores are read twice from tensor memory, 32 at a time and
+      // the next 32 in flight: for the maximum, then for the weights (held
+      // over instead, 128 of them spill).
+      const uint32_t sc = s_col[slot] + lanes;
+      uint32_t buf[2][32];
+      float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      auto hide = [&](uint32_t (&v)[32], int tok0) {
+        const uint32_t bits = mine.bits(tok0);
 #pragma unroll
-        for (int i = 0; i < KT; ++i)
-          if (!mine.has(t0 + i)) raw[i] = 0xff800000u;  // -inf
+        for (int e = 0; e < 32; ++e)
+          if (!(bits >> e & 1u)) v[e] = 0xff800000u;  // -inf
+      };
+      tmem_ld32_nowait(sc, buf[0]);
+#pragma unroll
+      for (int i = 0; i < KT / 32; ++i) {
+        uint32_t(&v)[32] = buf[i & 1];
+        tmem_wait_ld();
+        tmem_regs_after_wait<32>(v);
+        // (the last step starts the second reading)
+        tmem_ld32_nowait(sc + (i + 1 < KT / 32 ? 32 * (i + 1) : 0), buf[(i + 1) & 1]);
+        if (masked) hide(v, t0 + 32 * i);
+#pragma unroll
+        for (int e = 0; e < 32; e += 8)
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            top4[u] = max3(top4[u], __uint_as_float(v[e + 2 * u]), __uint_as_float(v[e + 2 * u + 1]));
       }
-      float top = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < KT; ++i) top = fmaxf(top, __uint_as_float(raw[i]));
+      const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
       const bool grow = (fmaxf(top, m) - m) * c > kGrow;  // (false for a row that saw nothing)
       if (__any_sync(0xffffffffu, grow)) {
         const float m2 = grow ? fmaxf(top, m) : m;
@@ -443,18 +486,17 @@ __global__ void __launch_bounds__(64 + 128 * NQ, 1)
         if (j > 0) {
           if (NQ == 1) {
             // (with two row tiles S of this tile was issued after P V of the last)
-            got = 0;
-            if (lane == 0)
-              got = mbar_wait_bounded(pv_done, static_cast<uint32_t>(j - 1) & 1u, p.wait_limit_ns,
-                                      p.status, 36) ? 1u : 0u;
-            got = __shfl_sync(0xffffffffu, got, 0);
-            if (!got) {
+            if (!mbar_wait_bounded(pv_done, static_cast<uint32_t>(j - 1) & 1u, p.wait_limit_ns,
+                                   p.status, 36)) {
+              tmem_wait_ld();  // (scores on their way to registers)
               ok = false;
               break;
             }
+            __syncwarp();
             tc_fence_after();
           }
           const uint32_t o = o_col + wg * o_cols + lanes;
+#pragma unroll 1
           for (uint32_t i = 0; i < o_cols; i += 32) {
             uint32_t v[32];
             tmem_ld16_nowait(o + i, v);
@@ -469,17 +511,31 @@ __global__ void __launch_bounds__(64 + 128 * NQ, 1)
         }
       }
       const float mc = m == -INFINITY ? 0.f : m * c;
-      float sum = 0.f;
+      const uint64_t c2 = pair_of(c, c), mc2 = pair_of(-mc, -mc);
+      uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
-      for (int i = 0; i < KT; i += 2) {
-        const float a = exp2_fast(fmaf(__uint_as_float(raw[i]), c, -mc));
-        const float b = exp2_fast(fmaf(__uint_as_float(raw[i + 1]), c, -mc));
-        sum += a + b;
-        raw[i / 2] = pack_bf16x2(a, b);
+      for (int i = 0; i < KT / 32; ++i) {
+        uint32_t(&v)[32] = buf[(KT / 32 + i) & 1];
+        tmem_wait_ld();
+        tmem_regs_after_wait<32>(v);
+        if (i + 1 < KT / 32) tmem_ld32_nowait(sc + 32 * (i + 1), buf[(KT / 32 + i + 1) & 1]);
+        if (masked) hide(v, t0 + 32 * i);
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const float2 x = unpair(
+              pair_fma(pair_of(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), c2, mc2));
+          const float a = exp2_fast(x.x), b = exp2_fast(x.y);
+          sum[(e / 2) & 1] = pair_add(sum[(e / 2) & 1], pair_of(a, b));
+          w[e / 2] = pack_bf16x2(a, b);
+        }
+        // (32 scores become 16 columns, always behind the scores read)
+        tmem_st16(sc + 16 * i, w);
       }
-      l += sum;
-#pragma unroll
-      for (int i = 0; i < KT / 2; i += 16) tmem_st16(s_col[slot] + lanes + i, raw + i);
+      {
+        const float2 x = unpair(pair_add(sum[0], sum[1]));
+        l += x.x + x.y;
+      }
       tmem_wait_st();
       if (wg == 0 && masked && !any.covers(t0, t0 + KT)) {
         // Values no query of the CTA sees may be anything (a slot never
@@ -488,12 +544,8 @@ __global__ void __launch_bounds__(64 + 128 * NQ, 1)
         const int pos = (NQ == 2 ? 2 * j + 1 : (j + 1 < nj ? j + 2 : nj) + j) * chunks;
         for (int ch = 0; ch < chunks; ++ch) {
           const int sl = (pos + ch) % stages;
-          got = 0;
-          if (lane == 0)
-            got = mbar_wait_bounded(&full[sl], static_cast<uint32_t>((pos + ch) / stages) & 1u,
-                                    p.wait_limit_ns, p.status, 37) ? 1u : 0u;
-          got = __shfl_sync(0xffffffffu, got, 0);
-          if (!got) {
+          if (!mbar_wait_bounded(&full[sl], static_cast<uint32_t>((pos + ch) / stages) & 1u,
+                                 p.wait_limit_ns, p.status, 37)) {
             ok = false;
             break;
           }
@@ -512,10 +564,8 @@ __global__ void __launch_bounds__(64 + 128 * NQ, 1)
       if (lane == 0) mbar_arrive(&p_ready[slot]);
     }
     if (nj > 0 && ok) {
-      uint32_t got = 0;
-      if (lane == 0)
-        got = mbar_wait_bounded(o_full, 0, p.wait_limit_ns, p.status, 38) ? 1u : 0u;
-      ok = __shfl_sync(0xffffffffu, got, 0) != 0;
+      ok = mbar_wait_bounded(o_full, 0, p.wait_limit_ns, p.status, 38);
+      __syncwarp();
       tc_fence_after();
     }
     __nv_bfloat16 *out = p.o + static_cast<long long>(it.seq) * p.o_seq +
@@ -561,7 +611,7 @@ __global__ void __launch_bounds__(64 + 128 * NQ, 1)
       // rank, rank + split, ...
       const int pitch = cs.d + 4;  // floats: rows start in different banks
       float *part = reinterpret_cast<float *>(smem);
-      if (warp >= 2) {
+      if (warp >= kFirstRowWarp) {
         const int r = (warp % 4) * 32 + lane;
         const uint32_t ml = smem_u32(row_ml) + 8u * r;
         float top = -INFINITY;
@@ -776,7 +826,7 @@ cudaError_t launch_attention(AttnArgs a, const void *q, const Strides &sq, const
   attr[1].val.clusterDim.x = static_cast<unsigned>(a.split);
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(64 + 128 * nq);
+  cfg.blockDim = dim3(attn_threads(nq));
   cfg.dynamicSmemBytes = smem(a.stages);
   cfg.stream = stream;
   cfg.attrs = attr;

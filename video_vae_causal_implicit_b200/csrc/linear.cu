@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_launch_dependents();
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       // both CTAs' loads complete on the leader's barriers, which the leader
       // arms for the bytes of both
       const uint32_t lead_full = PAIR ? mapa_shared(smem_u32(full), 0u) : 0u;
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (used >> i & 1u) mbar_wait_bounded(&full[i], par >> i & 1u, kDrainNs, nullptr, 0);
     }
   } else if (warp == 1) {
-    if (lane == 0 && leader) {
+    if (leader && elect_one()) {
       const uint32_t idesc = FP8 ? idesc_e4m3_f32(kRowsPerTile, p.nt)
                                  : idesc_bf16_f32(kRowsPerTile, p.nt);
       const uint64_t a0 = smem_desc_sw128(smem_base, 1024u);
@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(kSplitThreads)
   griddep_wait();
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       int s = 0;
       uint32_t ph = 0, used = 0, par = 0;
       for (int kc = k0; kc < k1; ++kc) {
@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(kSplitThreads)
         if (used >> i & 1u) mbar_wait_bounded(&full[i], par >> i & 1u, kDrainNs, nullptr, 0);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t idesc =
           FP8 ? idesc_e4m3_f32(kTileRows, p.nt) : idesc_bf16_f32(kTileRows, p.nt);
       const uint64_t a0 = smem_desc_sw128(smem_base, 1024u);
