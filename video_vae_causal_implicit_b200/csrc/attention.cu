@@ -173,9 +173,62 @@ __device__ __forceinline__ float exp2_fast(float x) {
 constexpr int kFirstRowWarp = 4;
 constexpr __host__ __device__ int attn_threads(int nq) { return 32 * kFirstRowWarp + 128 * nq; }
 // 168 registers a thread at launch with 384 threads; the row warps' tile of
-// scores wants more: 136 * 128 + 184 * 256 = 168 * 384.
-constexpr int kRegsFew = 136, kRegsMany = 184;
+// scores wants more: 88 * 128 + 208 * 256 = 168 * 384.
+constexpr int kRegsFew = 88, kRegsMany = 208;
+static_assert(kRegsFew * 128 + kRegsMany * 256 <= 168 * 384, "an increase past the launch's registers waits forever");
 
+// A row's scores of a key tile, all of them in registers on return.
+__device__ __forceinline__ void tmem_ld_all128(uint32_t taddr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%128];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%129];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95}, [%130];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%131];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+        "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]),
+        "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]),
+        "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
+        "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]),
+        "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]),
+        "=r"(r[61]), "=r"(r[62]), "=r"(r[63]), "=r"(r[64]), "=r"(r[65]), "=r"(r[66]),
+        "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]), "=r"(r[72]),
+        "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]), "=r"(r[78]),
+        "=r"(r[79]), "=r"(r[80]), "=r"(r[81]), "=r"(r[82]), "=r"(r[83]), "=r"(r[84]),
+        "=r"(r[85]), "=r"(r[86]), "=r"(r[87]), "=r"(r[88]), "=r"(r[89]), "=r"(r[90]),
+        "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]), "=r"(r[96]),
+        "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]), "=r"(r[102]),
+        "=r"(r[103]), "=r"(r[104]), "=r"(r[105]), "=r"(r[106]), "=r"(r[107]), "=r"(r[108]),
+        "=r"(r[109]), "=r"(r[110]), "=r"(r[111]), "=r"(r[112]), "=r"(r[113]), "=r"(r[114]),
+        "=r"(r[115]), "=r"(r[116]), "=r"(r[117]), "=r"(r[118]), "=r"(r[119]), "=r"(r[120]),
+        "=r"(r[121]), "=r"(r[122]), "=r"(r[123]), "=r"(r[124]), "=r"(r[125]), "=r"(r[126]),
+        "=r"(r[127])
+      : "r"(taddr + 0), "r"(taddr + 32), "r"(taddr + 64), "r"(taddr + 96)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_all64(uint32_t taddr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+        "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]),
+        "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]),
+        "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
+        "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]),
+        "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]),
+        "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr + 0), "r"(taddr + 32)
+      : "memory");
+}
 template <int NQ, int KT>
 __global__ void __launch_bounds__(attn_threads(NQ), 1)
     attn_kernel(const __grid_constant__ CUtensorMap map_q,
@@ -263,14 +316,10 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
   griddep_launch_dependents();
   bool ok = true;
 
-  if constexpr (NQ == 2) {
-    if (warp < kFirstRowWarp)
-      regs_fewer<kRegsFew>();
-    else
-      regs_more<kRegsMany>();
-  }
+  // (in the branches: code after a common point gets the smaller share)
   if (warp == 0) {
     // ------------------------------ loads ---------------------------------------
+    if constexpr (NQ == 2) regs_fewer<kRegsFew>();
     if (nj > 0 && elect_one()) {
       const int rows = p.tok_tile * p.group;
       mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(NQ * chunks * rows) * 128u);
@@ -308,6 +357,7 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
     }
   } else if (warp == 1) {
     // ------------------------------ products ------------------------------------
+    if constexpr (NQ == 2) regs_fewer<kRegsFew>();
     if (nj > 0 && elect_one()) {
       const uint32_t idesc_s = idesc_bf16_f32(kRows, KT);
       // O in steps of two chunks where they pair up in the ring
@@ -424,6 +474,7 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
     }
   } else if (warp >= kFirstRowWarp) {
     // ------------------------------ softmax, output ------------------------------
+    if constexpr (NQ == 2) regs_more<kRegsMany>();
     const int wg = (warp - kFirstRowWarp) / 4;  // this warp's row tile
     const int quarter = warp % 4;   // the tensor-memory lanes it may read
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
@@ -449,33 +500,25 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
       tc_fence_after();
       const int t0 = tiles.at(j0 + j) * KT;
       const bool masked = !every.covers(t0, t0 + KT);
-      // The row's scores are read twice from tensor memory, 32 at a time and
-      // the next 32 in flight: for the maximum, then for the weights (held
-      // over instead, 128 of them spill).
       const uint32_t sc = s_col[slot] + lanes;
-      uint32_t buf[2][32];
+      uint32_t raw[KT];
       float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      auto hide = [&](uint32_t (&v)[32], int tok0) {
+      auto hide = [&](uint32_t *v, int tok0) {
         const uint32_t bits = mine.bits(tok0);
 #pragma unroll
         for (int e = 0; e < 32; ++e)
           if (!(bits >> e & 1u)) v[e] = 0xff800000u;  // -inf
       };
-      tmem_ld32_nowait(sc, buf[0]);
+      if constexpr (KT == 128) tmem_ld_all128(sc, raw); else tmem_ld_all64(sc, raw);
+      if (masked) {
 #pragma unroll
-      for (int i = 0; i < KT / 32; ++i) {
-        uint32_t(&v)[32] = buf[i & 1];
-        tmem_wait_ld();
-        tmem_regs_after_wait<32>(v);
-        // (the last step starts the second reading)
-        tmem_ld32_nowait(sc + (i + 1 < KT / 32 ? 32 * (i + 1) : 0), buf[(i + 1) & 1]);
-        if (masked) hide(v, t0 + 32 * i);
-#pragma unroll
-        for (int e = 0; e < 32; e += 8)
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            top4[u] = max3(top4[u], __uint_as_float(v[e + 2 * u]), __uint_as_float(v[e + 2 * u + 1]));
+        for (int i = 0; i < KT; i += 32) hide(raw + i, t0 + i);
       }
+#pragma unroll
+      for (int e = 0; e < KT; e += 8)
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          top4[u] = max3(top4[u], __uint_as_float(raw[e + 2 * u]), __uint_as_float(raw[e + 2 * u + 1]));
       const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
       const bool grow = (fmaxf(top, m) - m) * c > kGrow;  // (false for a row that saw nothing)
       if (__any_sync(0xffffffffu, grow)) {
@@ -488,7 +531,6 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
             // (with two row tiles S of this tile was issued after P V of the last)
             if (!mbar_wait_bounded(pv_done, static_cast<uint32_t>(j - 1) & 1u, p.wait_limit_ns,
                                    p.status, 36)) {
-              tmem_wait_ld();  // (scores on their way to registers)
               ok = false;
               break;
             }
@@ -515,11 +557,7 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
       uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
       for (int i = 0; i < KT / 32; ++i) {
-        uint32_t(&v)[32] = buf[(KT / 32 + i) & 1];
-        tmem_wait_ld();
-        tmem_regs_after_wait<32>(v);
-        if (i + 1 < KT / 32) tmem_ld32_nowait(sc + 32 * (i + 1), buf[(KT / 32 + i + 1) & 1]);
-        if (masked) hide(v, t0 + 32 * i);
+        uint32_t *v = raw + 32 * i;
         uint32_t w[16];
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
@@ -601,6 +639,8 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
       }
     }
     if (split > 1) row_ml[r] = make_float2(m, l);
+  } else {
+    if constexpr (NQ == 2) regs_fewer<kRegsFew>();
   }
   if constexpr (NQ == 1) {
     if (split > 1) {
