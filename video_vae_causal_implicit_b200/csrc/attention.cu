@@ -137,13 +137,6 @@ struct TileList {
   }
 };
 
-// What one CTA (or cluster) works on.
-struct Item {
-  int seq, kv_head, tok0;  // first query token
-  int live;                // query tokens of the sequence (all frames of its chunk)
-  int base;                // frame of query token 0 (negative: seen by nothing)
-};
-
 __device__ __forceinline__ void lengths(const CacheShape &c, int seq, int &chunk, int &all) {
   all = c.k_frames ? c.k_frames[seq] : c.total;
   if (all < 0) all = 0;
@@ -152,15 +145,36 @@ __device__ __forceinline__ void lengths(const CacheShape &c, int seq, int &chunk
   chunk = chunk < 0 ? 0 : (chunk > c.t ? c.t : chunk);
 }
 
-template <int KT>
-__host__ __device__ inline uint32_t attn_bars_off(int nq, int chunks, int stages) {
-  return static_cast<uint32_t>(nq * chunks) * kQChunk + static_cast<uint32_t>(stages) * KT * 128u;
-}
-template <int KT>
-__host__ __device__ inline uint32_t attn_smem(int nq, int chunks, int stages) {
-  // barriers, and the rows' (maximum, sum) for a split
-  return attn_bars_off<KT>(nq, chunks, stages) + 8u * (2u * stages + 8u) + 16u + kRows * 8u + 1024u;
-}
+// Shapes of a kernel: NQ row tiles of 128, key tiles of KT tokens, CH chunks
+// of 64 channels.  Keys and values travel in groups of GC chunks (one
+// barrier, one N = 64 GC product step of P V), NG groups a tile.
+template <int NQ, int KT, int CH>
+struct Shape {
+  static constexpr int GC = CH <= 2 ? CH : CH / 2;
+  static constexpr int NG = CH / GC;
+  static constexpr uint32_t kChunk = KT * 128u;
+  static constexpr uint32_t kGroup = GC * kChunk;
+  static constexpr uint32_t kQ = NQ * CH * kQChunk;
+  // Shared memory: Q, the ring of groups (after them, in a split, the parts
+  // of the rows in their place), barriers, the rows' (maximum, sum).
+  static constexpr uint32_t rest(int stages) {
+    return 8u * (2u * stages + 3u + 5u * NQ) + 16u + NQ * kRows * 8u + 1024u;
+  }
+  static constexpr int stages() {
+    int st = 24;
+    while (kQ + st * kGroup + rest(st) > kSmemMost) --st;
+    return st;
+  }
+  static constexpr int kStages = stages();
+  static constexpr uint32_t kBars = kQ + kStages * kGroup;
+  static constexpr uint32_t kSmem = kBars + rest(kStages);
+  // tensor memory: two slots of scores and the output per row tile
+  static_assert(2 * NQ * KT + NQ * 64 * CH <= 512, "tensor memory columns");
+  // a value tile, the key tile two ahead and the value tile before fit at once
+  static_assert(kStages >= 3 * NG || (NQ == 1 && kStages >= 2 * NG), "ring depth");
+  // the parts of a split: rows of d + 4 floats
+  static_assert(NQ * kRows * (64 * CH + 4) * 4 <= kBars, "space for the parts of the rows");
+};
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -173,9 +187,10 @@ __device__ __forceinline__ float exp2_fast(float x) {
 constexpr int kFirstRowWarp = 4;
 constexpr __host__ __device__ int attn_threads(int nq) { return 32 * kFirstRowWarp + 128 * nq; }
 // 168 registers a thread at launch with 384 threads; the row warps' tile of
-// scores wants more: 88 * 128 + 208 * 256 = 168 * 384.
-constexpr int kRegsFew = 88, kRegsMany = 208;
-static_assert(kRegsFew * 128 + kRegsMany * 256 <= 168 * 384, "an increase past the launch's registers waits forever");
+// scores wants more.
+constexpr int kRegsFew = 152, kRegsMany = 176;
+static_assert(kRegsFew * 128 + kRegsMany * 256 <= 168 * 384,
+              "an increase past the launch's registers waits forever");
 
 // A row's scores of a key tile, all of them in registers on return.
 __device__ __forceinline__ void tmem_ld_all128(uint32_t taddr, uint32_t *r) {
@@ -229,57 +244,40 @@ __device__ __forceinline__ void tmem_ld_all64(uint32_t taddr, uint32_t *r) {
       : "r"(taddr + 0), "r"(taddr + 32)
       : "memory");
 }
-template <int NQ, int KT>
+// NQ row tiles of 128, key tiles of KT tokens.  Every row tile has two slots
+// for its scores, so that the scores of the next key tile are there when the
+// softmax of one ends.
+//
+// The products are issued so that one of Q K^T (both operands from shared
+// memory) alternates with ones of P V (P from tensor memory): measured alone,
+// M = 128 products of the first kind take N / 2 + 44 cycles, of the second
+// N / 2 + 10; alternating N / 2 each (the first kind loads its A under the
+// second's product).
+template <int NQ, int KT, int CH>
 __global__ void __launch_bounds__(attn_threads(NQ), 1)
     attn_kernel(const __grid_constant__ CUtensorMap map_q,
                 const __grid_constant__ CUtensorMap map_k,
                 const __grid_constant__ CUtensorMap map_v, const AttnArgs p) {
-  constexpr uint32_t kSlot = KT * 128u;  // 64 channels of a key tile
+  using S = Shape<NQ, KT, CH>;
+  constexpr int GC = S::GC, NG = S::NG, stages = S::kStages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const CacheShape &cs = p.c;
-  const int chunks = p.chunks, stages = p.stages, split = NQ == 1 ? p.split : 1;
-  uint64_t *full = reinterpret_cast<uint64_t *>(smem + attn_bars_off<KT>(NQ, chunks, stages));
+  const int split = p.split;
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + S::kBars);
   uint64_t *empty = full + stages;
   uint64_t *q_full = empty + stages;
-  uint64_t *s_full = q_full + 1;   // [2]
-  uint64_t *p_ready = s_full + 2;  // [2]
-  uint64_t *pv_done = p_ready + 2;
-  uint64_t *o_full = pv_done + 1;
+  uint64_t *s_full = q_full + 1;          // [NQ][2]
+  uint64_t *p_ready = s_full + 2 * NQ;    // [NQ][2]
+  uint64_t *pv_done = p_ready + 2 * NQ;   // [NQ]
+  uint64_t *o_full = pv_done + NQ;
   uint64_t *drain = o_full + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
-  float2 *row_ml = reinterpret_cast<float2 *>(tmem_slot + 2);  // [128] (split)
+  float2 *row_ml = reinterpret_cast<float2 *>(tmem_slot + 2);  // [NQ * 128] (split)
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-
-  // the lengths may come from an earlier kernel of the stream
-  griddep_wait();
-  Item it;
-  {
-    int i = static_cast<int>(blockIdx.x) / split;
-    it.kv_head = i % cs.kv_heads;
-    i /= cs.kv_heads;
-    it.seq = i % cs.n;
-    // the last query tiles see the most keys: first
-    it.tok0 = (p.q_tiles - 1 - i / cs.n) * (NQ * p.tok_tile);
-    int chunk, all;
-    lengths(cs, it.seq, chunk, all);
-    it.live = chunk * cs.frame;
-    it.base = all - chunk;
-  }
-  if (it.tok0 >= it.live) return;  // (the whole cluster)
-  const int tok_end = min(it.tok0 + NQ * p.tok_tile, it.live);  // of this CTA
-  const int qf0 = it.base + it.tok0 / cs.frame, qf1 = it.base + (tok_end - 1) / cs.frame;
-  const int reach = p.window > 0 ? p.window - 1 : INT32_MAX;  // frames back
-  auto back = [&](int qf) { return qf > reach ? qf - reach : 0; };
-  // keys that some query of the CTA sees, and keys that all of them see
-  const Ranges any = token_ranges(cs, back(qf0), qf1, qf1);
-  const Ranges every = token_ranges(cs, back(qf1), qf0, qf0);
-  const TileList<KT> tiles(any);
-  const int j0 = static_cast<int>(static_cast<long long>(tiles.total) * rank / split);
-  const int nj = static_cast<int>(static_cast<long long>(tiles.total) * (rank + 1) / split) - j0;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < stages; ++i) {
@@ -287,11 +285,11 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
       mbar_init(&empty[i], 1);
     }
     mbar_init(q_full, 1);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 2 * NQ; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_ready[i], 4);  // the warps of a row tile
     }
-    mbar_init(pv_done, 1);
+    for (int i = 0; i < NQ; ++i) mbar_init(&pv_done[i], 1);
     mbar_init(o_full, 1);
     mbar_init(drain, 1);
     fence_mbar_init();
@@ -308,48 +306,88 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const uint32_t smem_base = smem_u32(smem);
-  const uint32_t ring = smem_base + static_cast<uint32_t>(NQ * chunks) * kQChunk;
-  // tensor memory: S (and P in its place) of slot 0 and 1, then O of each row tile
-  const uint32_t s_col[2] = {tmem, tmem + KT};
-  const uint32_t o_cols = static_cast<uint32_t>(chunks) * 64u;
-  const uint32_t o_col = tmem + 2 * KT;
+  const uint32_t ring = smem_base + S::kQ;
+  // tensor memory: the slots of S (and P in its place), then O, per row tile
+  auto s_col = [&](int q, int slot) { return tmem + static_cast<uint32_t>((2 * q + slot) * KT); };
+  constexpr uint32_t o_cols = CH * 64u;
+  const uint32_t o_col = tmem + 2 * NQ * KT;
   griddep_launch_dependents();
+  // (the lengths too may come from an earlier kernel of the stream)
+  griddep_wait();
+
+  // What this CTA (or cluster) works on: query tokens tok0 .. tok_end - 1 of
+  // one sequence and kv head.
+  int kv_head, seq, tok0, tok_end, base;
+  {
+    int i = static_cast<int>(blockIdx.x) / split;
+    kv_head = i % cs.kv_heads;
+    i /= cs.kv_heads;
+    seq = i % cs.n;
+    // the last query tiles see the most keys: first
+    const int tile = p.q_tiles - 1 - i / cs.n;
+    int chunk, all;
+    lengths(cs, seq, chunk, all);
+    base = all - chunk;  // frame of query token 0 (negative: sees nothing)
+    tok_end = chunk * cs.frame;
+    if (p.tiles_frame > 0) {  // tiles that end with their frame
+      const int f = tile / p.tiles_frame;
+      tok0 = f * cs.frame + (tile - f * p.tiles_frame) * (NQ * p.tok_tile);
+      tok_end = min(tok_end, (f + 1) * cs.frame);
+    } else {
+      tok0 = tile * (NQ * p.tok_tile);
+    }
+    tok_end = min(tok_end, tok0 + NQ * p.tok_tile);  // (<= tok0: nothing to do)
+  }
+  const int reach = p.window > 0 ? p.window - 1 : INT32_MAX;  // frames back
+  auto back = [&](int qf) { return qf > reach ? qf - reach : 0; };
+  const int qf0 = base + tok0 / cs.frame;
+  const int qf1 = tok_end > tok0 ? base + (tok_end - 1) / cs.frame : -1;
+  // keys that some query of the CTA sees, and keys that all of them see
+  const Ranges any = token_ranges(cs, back(qf0), qf1, qf1);
+  const Ranges every = token_ranges(cs, back(qf1), qf1 < 0 ? -1 : qf0, qf1 < 0 ? -1 : qf0);
+  const TileList<KT> tiles(any);
+  const int j0 = static_cast<int>(static_cast<long long>(tiles.total) * rank / split);
+  const int nj = static_cast<int>(static_cast<long long>(tiles.total) * (rank + 1) / split) - j0;
   bool ok = true;
 
-  // (in the branches: code after a common point gets the smaller share)
+  // (registers move in the branches: code after a common point gets the
+  // smaller share)
   if (warp == 0) {
     // ------------------------------ loads ---------------------------------------
     if constexpr (NQ == 2) regs_fewer<kRegsFew>();
     if (nj > 0 && elect_one()) {
       const int rows = p.tok_tile * p.group;
-      mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(NQ * chunks * rows) * 128u);
+      mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(NQ * CH * rows) * 128u);
       for (int q = 0; q < NQ; ++q)
-        for (int c = 0; c < chunks; ++c)
-          tma_load_4d(smem_base + static_cast<uint32_t>(q * chunks + c) * kQChunk, &map_q, q_full,
-                      c * 64, it.kv_head * p.group, it.tok0 + q * p.tok_tile, it.seq);
+        for (int c = 0; c < CH; ++c)
+          tma_load_4d(smem_base + static_cast<uint32_t>(q * CH + c) * kQChunk, &map_q, q_full,
+                      c * 64, kv_head * p.group, tok0 + q * p.tok_tile, seq);
       int s = 0;
       uint32_t ph = 0, used = 0, par = 0;
       auto load = [&](const CUtensorMap *map, int j) {
         const int tok = tiles.at(j0 + j) * KT;
 #pragma unroll 1
-        for (int c = 0; c < chunks && ok; ++c) {
+        for (int g = 0; g < NG && ok; ++g) {
           if (!mbar_wait_bounded(&empty[s], ph ^ 1, p.wait_limit_ns, p.status, 30)) {
             ok = false;
             return;
           }
-          mbar_arrive_expect_tx(&full[s], kSlot);
+          mbar_arrive_expect_tx(&full[s], S::kGroup);
           used |= 1u << s;
           par = (par & ~(1u << s)) | (ph << s);
-          tma_load_4d(ring + s * kSlot, map, &full[s], c * 64, it.kv_head, tok, it.seq);
+#pragma unroll
+          for (int c = 0; c < GC; ++c)
+            tma_load_4d(ring + s * S::kGroup + c * S::kChunk, map, &full[s], (g * GC + c) * 64,
+                        kv_head, tok, seq);
           if (++s == stages) { s = 0; ph ^= 1; }
         }
       };
-      // in the order of their first use
+      // in the order of their first use: K 0, K 1, V 0, K 2, V 1, ...
       load(&map_k, 0);
+#pragma unroll 1
       for (int j = 0; j < nj && ok; ++j) {
-        if (NQ == 1 && j + 1 < nj) load(&map_k, j + 1);
+        if (j + 1 < nj) load(&map_k, j + 1);
         if (ok) load(&map_v, j);
-        if (NQ == 2 && ok && j + 1 < nj) load(&map_k, j + 1);
       }
       mbar_wait_bounded(q_full, 0, kDrainNs, nullptr, 0);
       for (int i = 0; i < stages; ++i)
@@ -359,114 +397,168 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
     // ------------------------------ products ------------------------------------
     if constexpr (NQ == 2) regs_fewer<kRegsFew>();
     if (nj > 0 && elect_one()) {
-      const uint32_t idesc_s = idesc_bf16_f32(kRows, KT);
-      // O in steps of two chunks where they pair up in the ring
-      const int wide = (chunks % 2 == 0 && stages % 2 == 0) ? 2 : 1;
-      const uint32_t idesc_o = idesc_bf16_f32_bt(kRows, 64 * wide);
+      constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, KT);
+      constexpr uint32_t idesc_o = idesc_bf16_f32_bt(kRows, 64 * GC);
       const uint64_t qd = smem_desc_sw128(smem_base, 1024u);
       const uint64_t kd = smem_desc_sw128(ring, 1024u);
-      const uint64_t vd = smem_desc_sw128_mn(ring, kSlot, 1024u);
-      int s = 0;  // ring position of the next load to be consumed
-      uint32_t ph = 0;
-      auto step = [&](int &slot, uint32_t &phase) {
-        if (++slot == stages) { slot = 0; phase ^= 1; }
+      const uint64_t vd = smem_desc_sw128_mn(ring, S::kChunk, 1024u);
+      // ring position of the first group of a tile
+      struct Pos {
+        int slot;
+        uint32_t phase;
       };
-      auto fail = [&]() { ok = false; };
-      // S[slot] = Q[q] K^T of the key tile at ring position (ks, kp)
-      auto qk = [&](int q, int slot, int ks, uint32_t kp, bool wait, bool release) {
-#pragma unroll 1
-        for (int c = 0; c < chunks; ++c) {
-          if (wait && !mbar_wait_bounded(&full[ks], kp, p.wait_limit_ns, p.status, 31))
-            return fail();
-          const uint64_t a = qd + ((static_cast<uint32_t>(q * chunks + c) * kQChunk) >> 4);
-          const uint64_t b = kd + ((ks * kSlot) >> 4);
+      auto next = [&](Pos x) {
+        if (++x.slot == stages) { x.slot = 0; x.phase ^= 1; }
+        return x;
+      };
+      auto advance = [&](Pos &x) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            umma_bf16(s_col[slot], a + 2 * i, b + 2 * i, idesc_s, c > 0 || i > 0);
-          if (release) umma_commit(&empty[ks]);
-          step(ks, kp);
-        }
-        umma_commit(&s_full[slot]);
+        for (int g = 0; g < NG; ++g) x = next(x);
       };
-      // O[q] (+)= P[slot] V of the value tile at ring position (vs, vp)
-      auto pv = [&](int q, int slot, int vs, uint32_t vp, bool wait, bool release, bool first) {
-#pragma unroll 1
-        for (int c = 0; c < chunks; c += wide) {
-          int v2 = vs;
-          uint32_t p2 = vp;
-          for (int u = 0; u < wide; ++u) {
-            if (wait && !mbar_wait_bounded(&full[v2], p2, p.wait_limit_ns, p.status, 32))
-              return fail();
-            step(v2, p2);
-          }
-          const uint64_t b = vd + ((vs * kSlot) >> 4);
-          const uint32_t d = o_col + q * o_cols + c * 64;
+      auto await = [&](uint64_t *bar, uint32_t parity, int site) {
+        if (ok && !mbar_wait_bounded(bar, parity, p.wait_limit_ns, p.status, site)) ok = false;
+        return ok;
+      };
+      auto await_tile = [&](Pos x, int site) {
 #pragma unroll
-          for (int i = 0; i < KT / 16; ++i)
-            umma_bf16_ta(d, s_col[slot] + 8 * i, b + 128 * i, idesc_o, !first || i > 0);
-          if (release) {
-            umma_commit(&empty[vs]);
-            if (wide == 2) umma_commit(&empty[vs + 1]);
-          }
-          vs = v2;
-          vp = p2;
+        for (int g = 0; g < NG; ++g) {
+          await(&full[x.slot], x.phase, site);
+          x = next(x);
         }
       };
-      auto wait_p = [&](int slot, uint32_t parity) {
-        if (!mbar_wait_bounded(&p_ready[slot], parity, p.wait_limit_ns, p.status, 33)) {
-          ok = false;
-          return;
-        }
-        tc_fence_after();
-      };
-      auto advance = [&]() {
-        s += chunks;
-        while (s >= stages) {
-          s -= stages;
-          ph ^= 1;
+      // (after the MMAs that read them)
+      auto release_tile = [&](Pos x) {
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          umma_commit(&empty[x.slot]);
+          x = next(x);
         }
       };
-      if (!mbar_wait_bounded(q_full, 0, p.wait_limit_ns, p.status, 34)) ok = false;
+      constexpr int kSteps = KT / 16;
+      // the i-th product of S[q][slot] = Q[q] K^T, of O[q] (+)= P[q][slot] V
+      struct Desc {
+        uint64_t d[NG];
+      };
+      auto desc_of = [&](uint64_t base_desc, Pos x) {
+        Desc r;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          r.d[g] = base_desc + ((x.slot * S::kGroup) >> 4);
+          x = next(x);
+        }
+        return r;
+      };
+      auto score_step = [&](int q, uint32_t col, const Desc &b, int i) {
+        const int c = i / 4, k = i % 4;
+        umma_bf16(col, qd + ((static_cast<uint32_t>(q * CH + c) * kQChunk) >> 4) + 2 * k,
+                  b.d[c / GC] + (((c % GC) * S::kChunk) >> 4) + 2 * k, idesc_s, i > 0);
+      };
+      auto value_step = [&](int q, uint32_t col, const Desc &b, int i, bool first) {
+        const int g = i / kSteps, k = i % kSteps;
+        umma_bf16_ta(o_col + q * o_cols + g * GC * 64, col + 8 * k, b.d[g] + 128 * k, idesc_o,
+                     !first || k > 0);
+      };
+      auto scores = [&](int q, int slot, Pos k) {
+        const Desc b = desc_of(kd, k);
+        const uint32_t col = s_col(q, slot);
+#pragma unroll
+        for (int i = 0; i < 4 * CH; ++i) score_step(q, col, b, i);
+        umma_commit(&s_full[2 * q + slot]);
+      };
+      auto values = [&](int q, int slot, Pos v, bool first) {
+        const Desc b = desc_of(vd, v);
+        const uint32_t col = s_col(q, slot);
+#pragma unroll
+        for (int i = 0; i < NG * kSteps; ++i) value_step(q, col, b, i, first);
+        umma_commit(&pv_done[q]);
+      };
+      // both, for different row tiles, alternating
+      auto scores_values = [&](int q, int slot, Pos k, int q2, int slot2, Pos v, bool first) {
+        const Desc b = desc_of(kd, k), b2 = desc_of(vd, v);
+        const uint32_t col = s_col(q, slot), col2 = s_col(q2, slot2);
+        constexpr int kS = 4 * CH, kV = NG * kSteps;
+#pragma unroll
+        for (int i = 0; i < kS; ++i) {
+          score_step(q, col, b, i);
+#pragma unroll
+          for (int u = i * kV / kS; u < (i + 1) * kV / kS; ++u) value_step(q2, col2, b2, u, first);
+        }
+        umma_commit(&s_full[2 * q + slot]);
+        umma_commit(&pv_done[q2]);
+      };
+      Pos at{0, 0};  // of the next tile in the ring
+      await(q_full, 0, 34);
+      await_tile(at, 31);
       if constexpr (NQ == 1) {
-        if (ok) qk(0, 0, s, ph, true, true);
-        advance();
-        for (int j = 0; j < nj && ok; ++j) {
-          if (j + 1 < nj) {
-            qk(0, (j + 1) & 1, s, ph, true, true);
-            advance();
-            if (!ok) break;
+        if (ok) {
+          scores(0, 0, at);
+          release_tile(at);
+          advance(at);
+        }
+        if (nj > 1) {
+          await_tile(at, 31);
+          if (ok) {
+            scores(0, 1, at);
+            release_tile(at);
+            advance(at);
           }
-          wait_p(j & 1, (j >> 1) & 1);
-          if (!ok) break;
-          pv(0, j & 1, s, ph, true, true, j == 0);
-          advance();
-          if (!ok) break;
-          umma_commit(pv_done);
+        }
+#pragma unroll 1
+        for (int j = 0; j < nj; ++j) {
+          await_tile(at, 32);
+          if (!await(&p_ready[j & 1], (j >> 1) & 1, 33)) break;
+          tc_fence_after();
+          values(0, j & 1, at, j == 0);
+          release_tile(at);
+          advance(at);
+          if (j + 2 < nj) {
+            await_tile(at, 31);
+            if (!ok) break;
+            scores(0, j & 1, at);
+            release_tile(at);
+            advance(at);
+          }
         }
       } else {
-        int vs = 0;  // the last value tile's position
-        uint32_t vp = 0;
-        for (int j = 0; j < nj && ok; ++j) {
-          const int ks = s;
-          const uint32_t kp = ph;
-          advance();
-          qk(0, 0, ks, kp, true, false);
-          if (!ok) break;
-          if (j > 0) {
-            wait_p(1, (j - 1) & 1);
-            if (!ok) break;
-            pv(1, 1, vs, vp, false, true, j == 1);
-          }
-          qk(1, 1, ks, kp, false, true);
-          wait_p(0, j & 1);
-          if (!ok) break;
-          vs = s;
-          vp = ph;
-          advance();
-          pv(0, 0, vs, vp, true, false, j == 0);
+        Pos k = at;  // the key tile whose scores of row tile 1 come next
+        if (ok) {
+          scores(0, 0, at);
+          scores(1, 0, at);
+          release_tile(at);
+          advance(at);
         }
-        if (ok) wait_p(1, (nj - 1) & 1);
-        if (ok) pv(1, 1, vs, vp, false, true, nj == 1);
+        if (nj > 1) {
+          await_tile(at, 31);
+          k = at;
+          if (ok) scores(0, 1, at);
+          advance(at);
+        }
+#pragma unroll 1
+        for (int j = 0; j < nj; ++j) {
+          // in the ring: V j at `at`, then K j + 2; K j + 1 at k
+          const Pos v = at;
+          advance(at);
+          await_tile(v, 32);
+          if (!await(&p_ready[j & 1], (j >> 1) & 1, 33)) break;
+          tc_fence_after();
+          if (j + 1 < nj) {
+            scores_values(1, (j + 1) & 1, k, 0, j & 1, v, j == 0);
+            release_tile(k);
+          } else {
+            values(0, j & 1, v, j == 0);
+          }
+          if (j + 2 < nj) await_tile(at, 31);
+          if (!await(&p_ready[2 + (j & 1)], (j >> 1) & 1, 33)) break;
+          tc_fence_after();
+          if (j + 2 < nj) {
+            k = at;
+            scores_values(0, j & 1, k, 1, j & 1, v, j == 0);
+            advance(at);
+          } else {
+            values(1, j & 1, v, j == 0);
+          }
+          release_tile(v);
+        }
       }
       if (ok) umma_commit(o_full);
       umma_commit(drain);
@@ -476,44 +568,44 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
     // ------------------------------ softmax, output ------------------------------
     if constexpr (NQ == 2) regs_more<kRegsMany>();
     const int wg = (warp - kFirstRowWarp) / 4;  // this warp's row tile
-    const int quarter = warp % 4;   // the tensor-memory lanes it may read
+    const int quarter = warp % 4;               // the tensor-memory lanes it may read
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const int r = quarter * 32 + lane;  // its row of the tile
-    const int tok = it.tok0 + wg * p.tok_tile + r / p.group;
-    const int head = it.kv_head * p.group + r % p.group;
-    const bool live = r < p.tok_tile * p.group && tok < it.live;
+    const int tok = tok0 + wg * p.tok_tile + r / p.group;
+    const int head = kv_head * p.group + r % p.group;
+    const bool live = r < p.tok_tile * p.group && tok < tok_end;
     Ranges mine;
     {
-      const int qf = it.base + tok / cs.frame;
-      mine = live ? token_ranges(cs, back(qf), qf, qf) : token_ranges(cs, 0, -1, -1);
+      const int qf = live ? base + tok / cs.frame : -1;
+      mine = token_ranges(cs, back(qf), qf, qf);
     }
     const float c = p.scale_log2;
     float m = -INFINITY, l = 0.f;  // the maximum that p is relative to, and sum of p
     for (int j = 0; j < nj; ++j) {
-      const int slot = NQ == 2 ? wg : (j & 1);
-      const uint32_t par = static_cast<uint32_t>(NQ == 2 ? j : (j >> 1)) & 1u;
-      if (!mbar_wait_bounded(&s_full[slot], par, p.wait_limit_ns, p.status, 35)) {
+      const int t0 = tiles.at(j0 + j) * KT;
+      const bool masked = !every.covers(t0, t0 + KT);
+      const int slot = j & 1;
+      if (!mbar_wait_bounded(&s_full[2 * wg + slot], static_cast<uint32_t>(j >> 1) & 1u,
+                             p.wait_limit_ns, p.status, 35)) {
         ok = false;
         break;
       }
       __syncwarp();
       tc_fence_after();
-      const int t0 = tiles.at(j0 + j) * KT;
-      const bool masked = !every.covers(t0, t0 + KT);
-      const uint32_t sc = s_col[slot] + lanes;
+      const uint32_t sc = s_col(wg, slot) + lanes;
       uint32_t raw[KT];
-      float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      auto hide = [&](uint32_t *v, int tok0) {
-        const uint32_t bits = mine.bits(tok0);
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-          if (!(bits >> e & 1u)) v[e] = 0xff800000u;  // -inf
-      };
-      if constexpr (KT == 128) tmem_ld_all128(sc, raw); else tmem_ld_all64(sc, raw);
+      if constexpr (KT == 128) tmem_ld_all128(sc, raw);
+      else tmem_ld_all64(sc, raw);
       if (masked) {
 #pragma unroll
-        for (int i = 0; i < KT; i += 32) hide(raw + i, t0 + i);
+        for (int i = 0; i < KT; i += 32) {
+          const uint32_t bits = mine.bits(t0 + i);
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (!(bits >> e & 1u)) raw[i + e] = 0xff800000u;  // -inf
+        }
       }
+      float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
       for (int e = 0; e < KT; e += 8)
 #pragma unroll
@@ -527,28 +619,24 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
         m = m2;
         l *= f;
         if (j > 0) {
-          if (NQ == 1) {
-            // (with two row tiles S of this tile was issued after P V of the last)
-            if (!mbar_wait_bounded(pv_done, static_cast<uint32_t>(j - 1) & 1u, p.wait_limit_ns,
-                                   p.status, 36)) {
-              ok = false;
-              break;
-            }
-            __syncwarp();
-            tc_fence_after();
+          // (the products of the tile before still add to O)
+          if (!mbar_wait_bounded(&pv_done[wg], static_cast<uint32_t>(j - 1) & 1u, p.wait_limit_ns,
+                                 p.status, 36)) {
+            ok = false;
+            break;
           }
+          __syncwarp();
+          tc_fence_after();
           const uint32_t o = o_col + wg * o_cols + lanes;
 #pragma unroll 1
           for (uint32_t i = 0; i < o_cols; i += 32) {
             uint32_t v[32];
-            tmem_ld16_nowait(o + i, v);
-            tmem_ld16_nowait(o + i + 16, v + 16);
+            tmem_ld32_nowait(o + i, v);
             tmem_wait_ld();
             tmem_regs_after_wait<32>(v);
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
-            tmem_st16(o + i, v);
-            tmem_st16(o + i + 16, v + 16);
+            tmem_st32(o + i, v);
           }
         }
       }
@@ -556,19 +644,17 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
       const uint64_t c2 = pair_of(c, c), mc2 = pair_of(-mc, -mc);
       uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
-      for (int i = 0; i < KT / 32; ++i) {
-        uint32_t *v = raw + 32 * i;
+      for (int i = 0; i < KT; i += 32) {
         uint32_t w[16];
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
-          const float2 x = unpair(
-              pair_fma(pair_of(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), c2, mc2));
+          const float2 x = unpair(pair_fma(
+              pair_of(__uint_as_float(raw[i + e]), __uint_as_float(raw[i + e + 1])), c2, mc2));
           const float a = exp2_fast(x.x), b = exp2_fast(x.y);
           sum[(e / 2) & 1] = pair_add(sum[(e / 2) & 1], pair_of(a, b));
           w[e / 2] = pack_bf16x2(a, b);
         }
-        // (32 scores become 16 columns, always behind the scores read)
-        tmem_st16(sc + 16 * i, w);
+        tmem_st16(sc + i / 2, w);
       }
       {
         const float2 x = unpair(pair_add(sum[0], sum[1]));
@@ -578,20 +664,23 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
       if (wg == 0 && masked && !any.covers(t0, t0 + KT)) {
         // Values no query of the CTA sees may be anything (a slot never
         // written, a frame beyond the end): 0 times a NaN would reach the
-        // sums, so their rows are cleared before the product reads them.
-        const int pos = (NQ == 2 ? 2 * j + 1 : (j + 1 < nj ? j + 2 : nj) + j) * chunks;
-        for (int ch = 0; ch < chunks; ++ch) {
-          const int sl = (pos + ch) % stages;
-          if (!mbar_wait_bounded(&full[sl], static_cast<uint32_t>((pos + ch) / stages) & 1u,
+        // sums, so their rows are cleared before the products read them (the
+        // first row tile's come first).
+        const int pos = ((j + 1 < nj ? j + 2 : nj) + j) * NG;
+        for (int g = 0; g < NG; ++g) {
+          const int sl = (pos + g) % stages;
+          if (!mbar_wait_bounded(&full[sl], static_cast<uint32_t>((pos + g) / stages) & 1u,
                                  p.wait_limit_ns, p.status, 37)) {
             ok = false;
             break;
           }
           if (r < KT && !any.has(t0 + r)) {
-            uint4 *row = reinterpret_cast<uint4 *>(
-                smem + static_cast<uint32_t>(NQ * chunks) * kQChunk + sl * kSlot + r * 128);
+            uint4 *row =
+                reinterpret_cast<uint4 *>(smem + S::kQ + sl * S::kGroup + r * 128);
+            for (int c = 0; c < GC; ++c)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) row[e] = make_uint4(0, 0, 0, 0);
+              for (int e = 0; e < 8; ++e)
+                row[c * (S::kChunk / 16) + e] = make_uint4(0, 0, 0, 0);
           }
         }
         if (!ok) break;
@@ -599,34 +688,34 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&p_ready[slot]);
+      if (lane == 0) mbar_arrive(&p_ready[2 * wg + slot]);
     }
     if (nj > 0 && ok) {
       ok = mbar_wait_bounded(o_full, 0, p.wait_limit_ns, p.status, 38);
       __syncwarp();
       tc_fence_after();
     }
-    __nv_bfloat16 *out = p.o + static_cast<long long>(it.seq) * p.o_seq +
-                         static_cast<long long>(tok) * p.o_tok +
-                         static_cast<long long>(head) * p.o_head;
     if (split == 1 && ok) {
-      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+      __nv_bfloat16 *out = p.o + static_cast<long long>(seq) * p.o_seq +
+                           static_cast<long long>(tok) * p.o_tok +
+                           static_cast<long long>(head) * p.o_head;
+      const float inv = (l > 0.f || l != l) ? 1.f / l : 0.f;
       const uint32_t o = o_col + wg * o_cols + lanes;
-      for (int i = 0; i < cs.d; i += 16) {
+      for (int i = 0; i < cs.d; i += 32) {
         __syncwarp();
-        uint32_t v[16];
+        uint32_t v[32];
         if (nj > 0) {
-          tmem_ld16_nowait(o + i, v);
+          tmem_ld32_nowait(o + i, v);
           tmem_wait_ld();
-          tmem_regs_after_wait<16>(v);
+          tmem_regs_after_wait<32>(v);
         }
         // (a row that saw nothing gives zeros, whatever the accumulator holds)
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
+        for (int e = 0; e < 32; ++e)
           v[e] = inv == 0.f ? 0u : __float_as_uint(__uint_as_float(v[e]) * inv);
         if (live) {
 #pragma unroll
-          for (int h = 0; h < 16; h += 8) {
+          for (int h = 0; h < 32; h += 8) {
             if (i + h >= cs.d) break;
             uint4 w;
             w.x = pack_bf16x2(__uint_as_float(v[h]), __uint_as_float(v[h + 1]));
@@ -638,84 +727,85 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
         }
       }
     }
-    if (split > 1) row_ml[r] = make_float2(m, l);
+    if (split > 1) row_ml[wg * kRows + r] = make_float2(m, l);
   } else {
     if constexpr (NQ == 2) regs_fewer<kRegsFew>();
   }
-  if constexpr (NQ == 1) {
-    if (split > 1) {
-      __syncwarp();
-      cluster_sync();
-      // Every rank scales its part by its share of the whole row, leaves it
-      // in its shared memory (the keys are done with), and finishes the rows
-      // rank, rank + split, ...
-      const int pitch = cs.d + 4;  // floats: rows start in different banks
-      float *part = reinterpret_cast<float *>(smem);
-      if (warp >= kFirstRowWarp) {
-        const int r = (warp % 4) * 32 + lane;
-        const uint32_t ml = smem_u32(row_ml) + 8u * r;
-        float top = -INFINITY;
-        for (int k = 0; k < split; ++k)
-          top = fmaxf(top, ld_cluster_f32x2(mapa_shared(ml, k)).x);
-        float all = 0.f;
-        for (int k = 0; k < split; ++k) {
-          const float2 v = ld_cluster_f32x2(mapa_shared(ml, k));
-          if (v.x != -INFINITY) all += v.y * exp2_fast((v.x - top) * p.scale_log2);
+  if (split > 1) {
+    __syncwarp();
+    cluster_sync();
+    // Every rank scales its part by its share of the whole row, leaves it in
+    // its shared memory (the keys are done with), and finishes the rows rank,
+    // rank + split, ...
+    const int pitch = cs.d + 4;  // floats: rows start in different banks
+    float *part = reinterpret_cast<float *>(smem);
+    const int tile_rows = p.tok_tile * p.group;  // used rows of a row tile
+    if (warp >= kFirstRowWarp) {
+      const int wg = (warp - kFirstRowWarp) / 4;
+      const int r = (warp % 4) * 32 + lane;
+      const uint32_t ml = smem_u32(row_ml) + 8u * (wg * kRows + r);
+      float top = -INFINITY;
+      for (int k = 0; k < split; ++k) top = fmaxf(top, ld_cluster_f32x2(mapa_shared(ml, k)).x);
+      float all = 0.f;
+      for (int k = 0; k < split; ++k) {
+        const float2 v = ld_cluster_f32x2(mapa_shared(ml, k));
+        if (v.x != -INFINITY) all += v.y * exp2_fast((v.x - top) * p.scale_log2);
+      }
+      const float2 me = row_ml[wg * kRows + r];
+      float f = 0.f;
+      if (me.x != -INFINITY && (all > 0.f || all != all))
+        f = exp2_fast((me.x - top) * p.scale_log2) / all;
+      const uint32_t o =
+          o_col + wg * o_cols + (static_cast<uint32_t>((warp % 4) * 32) << 16);
+      const bool have = ok && nj > 0;
+      float *dst = part + (wg * kRows + r) * pitch;
+      for (int i = 0; i < cs.d; i += 16) {
+        __syncwarp();
+        uint32_t v[16];
+        if (have) {
+          tmem_ld16_nowait(o + i, v);
+          tmem_wait_ld();
+          tmem_regs_after_wait<16>(v);
         }
-        const float2 me = row_ml[r];
-        float f = 0.f;
-        if (me.x != -INFINITY && (all > 0.f || all != all))
-          f = exp2_fast((me.x - top) * p.scale_log2) / all;
-        const uint32_t o = o_col + (static_cast<uint32_t>((warp % 4) * 32) << 16);
-        if (ok && nj > 0) {
-          for (int i = 0; i < cs.d; i += 8) {
-            __syncwarp();
-            uint32_t v[16];
-            tmem_ld16_nowait(o + (i & ~15), v);
-            tmem_wait_ld();
-            tmem_regs_after_wait<16>(v);
-            float4 w[2];
-            float *wf = reinterpret_cast<float *>(w);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float x = __uint_as_float((i & 8) ? v[8 + e] : v[e]);
-              wf[e] = f == 0.f ? 0.f : x * f;
-            }
-            float4 *dst = reinterpret_cast<float4 *>(part + r * pitch + i);
-            dst[0] = w[0];
-            dst[1] = w[1];
-          }
-        } else {
-          for (int i = 0; i < cs.d; i += 4)
-            *reinterpret_cast<float4 *>(part + r * pitch + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int e = 0; e < 16; ++e)
+          v[e] = (have && f != 0.f) ? __float_as_uint(__uint_as_float(v[e]) * f) : 0u;
+        if (r < tile_rows) {
+#pragma unroll
+          for (int e = 0; e < 16; e += 4)
+            if (i + e < cs.d)
+              *reinterpret_cast<uint4 *>(dst + i + e) =
+                  make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
         }
       }
-      __syncwarp();
-      cluster_sync();
-      const int rows = min(kRows / p.group * p.group, (tok_end - it.tok0) * p.group);
-      const int per = cs.d / 4;
-      const int mine = (rows - rank + split - 1) / split;  // rows this rank finishes
-      for (int x = threadIdx.x; x < mine * per; x += blockDim.x) {
-        const int r = rank + x / per * split, i = (x % per) * 4;
-        const uint32_t at = smem_base + static_cast<uint32_t>(r * pitch + i) * 4u;
-        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = 0; k < split; ++k) {
-          const uint32_t from = mapa_shared(at, k);
-          const float2 a = ld_cluster_f32x2(from), b = ld_cluster_f32x2(from + 8);
-          sum.x += a.x;
-          sum.y += a.y;
-          sum.z += b.x;
-          sum.w += b.y;
-        }
-        uint2 w;
-        w.x = pack_bf16x2(sum.x, sum.y);
-        w.y = pack_bf16x2(sum.z, sum.w);
-        *reinterpret_cast<uint2 *>(p.o + static_cast<long long>(it.seq) * p.o_seq +
-                                   static_cast<long long>(it.tok0 + r / p.group) * p.o_tok +
-                                   static_cast<long long>(it.kv_head * p.group + r % p.group) *
-                                       p.o_head +
-                                   i) = w;
+    }
+    __syncwarp();
+    cluster_sync();
+    const int rows = max(0, tok_end - tok0) * p.group;  // rows of all row tiles
+    const int per = cs.d / 4;
+    const int count = (rows - rank + split - 1) / split;  // this rank's
+    for (int x = threadIdx.x; x < count * per; x += blockDim.x) {
+      const int row = rank + x / per * split, i = (x % per) * 4;
+      const int q = row / tile_rows, r = row - q * tile_rows;
+      const uint32_t at =
+          smem_base + static_cast<uint32_t>((q * kRows + r) * pitch + i) * 4u;
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < split; ++k) {
+        const uint32_t from = mapa_shared(at, k);
+        const float2 a = ld_cluster_f32x2(from), b = ld_cluster_f32x2(from + 8);
+        sum.x += a.x;
+        sum.y += a.y;
+        sum.z += b.x;
+        sum.w += b.y;
       }
+      uint2 w;
+      w.x = pack_bf16x2(sum.x, sum.y);
+      w.y = pack_bf16x2(sum.z, sum.w);
+      *reinterpret_cast<uint2 *>(p.o + static_cast<long long>(seq) * p.o_seq +
+                                 static_cast<long long>(tok0 + row / p.group) * p.o_tok +
+                                 static_cast<long long>(kv_head * p.group + row % p.group) *
+                                     p.o_head +
+                                 i) = w;
     }
   }
   tc_fence_before();
@@ -786,7 +876,8 @@ cudaError_t prepare_kernels() {
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lk(mu);
   if (done[dev]) return cudaSuccess;
-  const AttnKernel ks[3] = {attn_kernel<2, 128>, attn_kernel<1, 128>, attn_kernel<1, 64>};
+  const AttnKernel ks[6] = {attn_kernel<2, 64, 1>,  attn_kernel<2, 64, 2>, attn_kernel<1, 128, 1>,
+                            attn_kernel<1, 128, 2>, attn_kernel<1, 64, 4>, attn_kernel<1, 64, 6>};
   for (const AttnKernel k : ks) {
     e = cudaFuncSetAttribute(reinterpret_cast<const void *>(k),
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -820,24 +911,43 @@ cudaError_t launch_attention(AttnArgs a, const void *q, const Strides &sq, const
   const CacheShape &c = a.c;
   a.group = a.heads / c.kv_heads;
   a.tok_tile = kRows / a.group;
-  a.chunks = (c.d + 63) / 64;
   const long long tokens = static_cast<long long>(c.t) * c.frame;
-  const long long tiles = (tokens + a.tok_tile - 1) / a.tok_tile;  // of 128 rows, per head
   const long long heads = static_cast<long long>(c.n) * c.kv_heads;
+  // frames that a query sees
+  const long long seen = a.window > 0 ? static_cast<long long>(a.window) + c.sinks : c.slots;
+  // Row tiles of a CTA, its query tokens, and the tiles of a chunk.  Tiles
+  // that cross frames see the keys of all of their frames; tiles that end
+  // with their frame leave rows unused: whichever reads fewer keys.
+  auto tile_count = [&](int nq, int *per_frame) {
+    const long long rows = static_cast<long long>(nq) * a.tok_tile;
+    const long long across = (tokens + rows - 1) / rows;
+    const long long within = (c.frame + rows - 1) / rows;
+    const double cost_across = static_cast<double>(across) * (seen + (rows - 1.0) / c.frame);
+    const double cost_within = static_cast<double>(c.t) * within * seen;
+    if (c.t > 1 && cost_within < cost_across) {
+      *per_frame = static_cast<int>(within);
+      return c.t * within;
+    }
+    *per_frame = 0;
+    return across;
+  };
   // Two row tiles a CTA (a key tile read once for both, one's softmax under
   // the other's products) when that still gives every SM a CTA; their
   // accumulators fit up to d = 128.
-  const bool two = c.d <= 128 && (tiles + 1) / 2 * heads >= sm_count / 2 && tiles > 1;
-  const int kt = c.d <= 128 ? 128 : 64;
+  int per_frame = 0;
+  const long long tiles1 = tile_count(1, &per_frame);
+  long long q_tiles = tile_count(2, &per_frame);
+  const bool two = c.d <= 128 && q_tiles * heads >= sm_count / 2 && tiles1 > 1;
+  if (!two) q_tiles = tile_count(1, &per_frame);
   const int nq = two ? 2 : 1;
-  const long long q_tiles = (tiles + nq - 1) / nq;
+  const int kt = (c.d <= 128 && !two) ? 128 : 64;
   a.q_tiles = static_cast<int>(q_tiles);
+  a.tiles_frame = per_frame;
   a.split = 1;
   if (!two) {
     // keys split over a cluster until every SM has a part of two tiles or more
-    const long long seen = a.window > 0 ? static_cast<long long>(a.window) + c.t - 1 + c.sinks
-                                        : c.slots;
-    const long long keys = (seen < c.slots ? seen : c.slots) * c.frame;
+    const long long most = (a.window > 0 ? seen + c.t - 1 : seen);
+    const long long keys = (most < c.slots ? most : c.slots) * c.frame;
     const long long key_tiles = (keys + kt - 1) / kt;
     while (a.split < 8 && (a.split + 1) * q_tiles * heads <= sm_count &&
            key_tiles >= 2 * (a.split + 1))
@@ -845,19 +955,23 @@ cudaError_t launch_attention(AttnArgs a, const void *q, const Strides &sq, const
   }
   const long long grid = q_tiles * heads * a.split;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
-  auto smem = [&](int st) {
-    return kt == 128 ? attn_smem<128>(nq, a.chunks, st) : attn_smem<64>(nq, a.chunks, st);
-  };
-  a.stages = 16;
-  while (a.stages > 2 && smem(a.stages) > kSmemMost) a.stages -= 2;
   CUtensorMap mq, mk, mv;
   const long long cached = static_cast<long long>(c.slots) * c.frame;
   if (!encode_heads(&mq, q, c.d, a.heads, tokens, c.n, sq, a.group, a.tok_tile) ||
       !encode_heads(&mk, k, c.d, c.kv_heads, cached, c.n, sk, 1, kt) ||
       !encode_heads(&mv, v, c.d, c.kv_heads, cached, c.n, sv, 1, kt))
     return cudaErrorInvalidValue;
-  const AttnKernel kern = two ? attn_kernel<2, 128>
-                              : (kt == 128 ? attn_kernel<1, 128> : attn_kernel<1, 64>);
+  // (channels are padded with zeros to whole chunks of the kernel's shape)
+  AttnKernel kern;
+  uint32_t smem;
+#define CC3D_ATTN(...) (kern = attn_kernel<__VA_ARGS__>, smem = Shape<__VA_ARGS__>::kSmem)
+  if (two && c.d <= 64) CC3D_ATTN(2, 64, 1);
+  else if (two) CC3D_ATTN(2, 64, 2);
+  else if (c.d <= 64) CC3D_ATTN(1, 128, 1);
+  else if (c.d <= 128) CC3D_ATTN(1, 128, 2);
+  else if (c.d <= 256) CC3D_ATTN(1, 64, 4);
+  else CC3D_ATTN(1, 64, 6);
+#undef CC3D_ATTN
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -867,7 +981,7 @@ cudaError_t launch_attention(AttnArgs a, const void *q, const Strides &sq, const
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(attn_threads(nq));
-  cfg.dynamicSmemBytes = smem(a.stages);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = a.split > 1 ? 2 : 1;

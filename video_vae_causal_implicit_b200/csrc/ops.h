@@ -89,7 +89,9 @@ struct AttnArgs {
   int *status;
   unsigned long long wait_limit_ns;
   int group, tok_tile;     // query heads per kv head; tokens per 128 rows
-  int chunks, stages, split, q_tiles;  // set by launch_attention
+  // set by launch_attention; tiles_frame: query tiles of a frame, 0 where tiles
+  // cross frames
+  int split, q_tiles, tiles_frame;
 };
 struct Strides {
   long long seq, tok, head;  // in elements
