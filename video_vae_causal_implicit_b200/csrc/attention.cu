@@ -158,7 +158,7 @@ struct Shape {
   // Shared memory: Q, the ring of groups (after them, in a split, the parts
   // of the rows in their place), barriers, the rows' (maximum, sum).
   static constexpr uint32_t rest(int stages) {
-    return 8u * (2u * stages + 3u + 5u * NQ) + 16u + NQ * kRows * 8u + 1024u;
+    return 8u * (2u * stages + 4u + 6u * NQ) + 16u + NQ * kRows * 8u + 1024u;
   }
   static constexpr int stages() {
     int st = 24;
@@ -182,7 +182,7 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// Warps 0 - 3: loads, products, two idle ones (the registers of a warpgroup
+// Warps 0 - 3: loads, products (two), an idle one (the registers of a warpgroup
 // can be moved only together); then four warps per row tile.
 constexpr int kFirstRowWarp = 4;
 constexpr __host__ __device__ int attn_threads(int nq) { return 32 * kFirstRowWarp + 128 * nq; }
@@ -248,11 +248,12 @@ __device__ __forceinline__ void tmem_ld_all64(uint32_t taddr, uint32_t *r) {
 // for its scores, so that the scores of the next key tile are there when the
 // softmax of one ends.
 //
-// The products are issued so that one of Q K^T (both operands from shared
-// memory) alternates with ones of P V (P from tensor memory): measured alone,
-// M = 128 products of the first kind take N / 2 + 44 cycles, of the second
-// N / 2 + 10; alternating N / 2 each (the first kind loads its A under the
-// second's product).
+// Measured alone, M = 128 products with both operands in shared memory (Q K^T)
+// take N / 2 + 44 cycles, with A in tensor memory (P V) N / 2 + 10, and
+// alternating N / 2 each: the first kind loads its A under the second's
+// product.  One thread cannot issue them that fast (a barrier wait costs it
+// some 130 cycles, a product 40), so two warps do: one per row tile, or one
+// per kind.
 template <int NQ, int KT, int CH>
 __global__ void __launch_bounds__(attn_threads(NQ), 1)
     attn_kernel(const __grid_constant__ CUtensorMap map_q,
@@ -270,10 +271,10 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
   uint64_t *q_full = empty + stages;
   uint64_t *s_full = q_full + 1;          // [NQ][2]
   uint64_t *p_ready = s_full + 2 * NQ;    // [NQ][2]
-  uint64_t *pv_done = p_ready + 2 * NQ;   // [NQ]
-  uint64_t *o_full = pv_done + NQ;
-  uint64_t *drain = o_full + 1;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+  uint64_t *pv_done = p_ready + 2 * NQ;   // [NQ][2]
+  uint64_t *o_full = pv_done + 2 * NQ;
+  uint64_t *drain = o_full + 1;           // [2]
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 2);
   float2 *row_ml = reinterpret_cast<float2 *>(tmem_slot + 2);  // [NQ * 128] (split)
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -282,16 +283,17 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < stages; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], NQ);  // (each row tile's products)
     }
     mbar_init(q_full, 1);
     for (int i = 0; i < 2 * NQ; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_ready[i], 4);  // the warps of a row tile
+      mbar_init(&pv_done[i], 1);
     }
-    for (int i = 0; i < NQ; ++i) mbar_init(&pv_done[i], 1);
-    mbar_init(o_full, 1);
-    mbar_init(drain, 1);
+    mbar_init(o_full, NQ);
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
     fence_mbar_init();
     prefetch_tmap(&map_q);
     prefetch_tmap(&map_k);
@@ -393,7 +395,7 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
       for (int i = 0; i < stages; ++i)
         if (used >> i & 1u) mbar_wait_bounded(&full[i], par >> i & 1u, kDrainNs, nullptr, 0);
     }
-  } else if (warp == 1) {
+  } else if (warp <= 2) {
     // ------------------------------ products ------------------------------------
     if constexpr (NQ == 2) regs_fewer<kRegsFew>();
     if (nj > 0 && elect_one()) {
@@ -411,9 +413,9 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
         if (++x.slot == stages) { x.slot = 0; x.phase ^= 1; }
         return x;
       };
-      auto advance = [&](Pos &x) {
-#pragma unroll
-        for (int g = 0; g < NG; ++g) x = next(x);
+      auto advance = [&](Pos &x, int n) {
+        x.slot += n * NG;
+        if (x.slot >= stages) { x.slot -= stages; x.phase ^= 1; }
       };
       auto await = [&](uint64_t *bar, uint32_t parity, int site) {
         if (ok && !mbar_wait_bounded(bar, parity, p.wait_limit_ns, p.status, site)) ok = false;
@@ -470,99 +472,63 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
         const uint32_t col = s_col(q, slot);
 #pragma unroll
         for (int i = 0; i < NG * kSteps; ++i) value_step(q, col, b, i, first);
-        umma_commit(&pv_done[q]);
+        umma_commit(&pv_done[2 * q + slot]);
       };
-      // both, for different row tiles, alternating
-      auto scores_values = [&](int q, int slot, Pos k, int q2, int slot2, Pos v, bool first) {
-        const Desc b = desc_of(kd, k), b2 = desc_of(vd, v);
-        const uint32_t col = s_col(q, slot), col2 = s_col(q2, slot2);
-        constexpr int kS = 4 * CH, kV = NG * kSteps;
-#pragma unroll
-        for (int i = 0; i < kS; ++i) {
-          score_step(q, col, b, i);
-#pragma unroll
-          for (int u = i * kV / kS; u < (i + 1) * kV / kS; ++u) value_step(q2, col2, b2, u, first);
-        }
-        umma_commit(&s_full[2 * q + slot]);
-        umma_commit(&pv_done[q2]);
-      };
-      Pos at{0, 0};  // of the next tile in the ring
       await(q_full, 0, 34);
-      await_tile(at, 31);
-      if constexpr (NQ == 1) {
-        if (ok) {
-          scores(0, 0, at);
-          release_tile(at);
-          advance(at);
-        }
-        if (nj > 1) {
-          await_tile(at, 31);
-          if (ok) {
-            scores(0, 1, at);
-            release_tile(at);
-            advance(at);
-          }
+      // the ring holds K 0, K 1, V 0, K 2, V 1, ...
+      Pos k{0, 0}, v{0, 0};
+      advance(v, nj > 1 ? 2 : 1);
+      if (NQ == 2) {
+        // each row tile's products from a warp of their own
+        const int q = warp - 1;
+        for (int j = 0; j < 2 && j < nj && ok; ++j) {
+          await_tile(k, 31);
+          if (!ok) break;
+          scores(q, j, k);
+          release_tile(k);
+          advance(k, 1 + j);  // (past V 0)
         }
 #pragma unroll 1
-        for (int j = 0; j < nj; ++j) {
-          await_tile(at, 32);
-          if (!await(&p_ready[j & 1], (j >> 1) & 1, 33)) break;
+        for (int j = 0; j < nj && ok; ++j) {
+          await_tile(v, 32);
+          if (j + 2 < nj) await_tile(k, 31);
+          if (!await(&p_ready[2 * q + (j & 1)], (j >> 1) & 1, 33)) break;
           tc_fence_after();
-          values(0, j & 1, at, j == 0);
-          release_tile(at);
-          advance(at);
+          values(q, j & 1, v, j == 0);
+          release_tile(v);
+          advance(v, j + 2 < nj ? 2 : 1);
           if (j + 2 < nj) {
-            await_tile(at, 31);
-            if (!ok) break;
-            scores(0, j & 1, at);
-            release_tile(at);
-            advance(at);
+            scores(q, j & 1, k);
+            release_tile(k);
+            advance(k, 2);
           }
+        }
+      } else if (warp == 1) {
+        // the two kinds of products from a warp each
+#pragma unroll 1
+        for (int j = 0; j < nj && ok; ++j) {
+          await_tile(k, 31);
+          if (j >= 2 && !await(&pv_done[j & 1], ((j >> 1) - 1) & 1, 39)) break;
+          if (!ok) break;
+          tc_fence_after();
+          scores(0, j & 1, k);
+          release_tile(k);
+          advance(k, j == 0 ? 1 : 2);
         }
       } else {
-        Pos k = at;  // the key tile whose scores of row tile 1 come next
-        if (ok) {
-          scores(0, 0, at);
-          scores(1, 0, at);
-          release_tile(at);
-          advance(at);
-        }
-        if (nj > 1) {
-          await_tile(at, 31);
-          k = at;
-          if (ok) scores(0, 1, at);
-          advance(at);
-        }
 #pragma unroll 1
-        for (int j = 0; j < nj; ++j) {
-          // in the ring: V j at `at`, then K j + 2; K j + 1 at k
-          const Pos v = at;
-          advance(at);
+        for (int j = 0; j < nj && ok; ++j) {
           await_tile(v, 32);
           if (!await(&p_ready[j & 1], (j >> 1) & 1, 33)) break;
           tc_fence_after();
-          if (j + 1 < nj) {
-            scores_values(1, (j + 1) & 1, k, 0, j & 1, v, j == 0);
-            release_tile(k);
-          } else {
-            values(0, j & 1, v, j == 0);
-          }
-          if (j + 2 < nj) await_tile(at, 31);
-          if (!await(&p_ready[2 + (j & 1)], (j >> 1) & 1, 33)) break;
-          tc_fence_after();
-          if (j + 2 < nj) {
-            k = at;
-            scores_values(0, j & 1, k, 1, j & 1, v, j == 0);
-            advance(at);
-          } else {
-            values(1, j & 1, v, j == 0);
-          }
+          values(0, j & 1, v, j == 0);
           release_tile(v);
+          advance(v, j + 2 < nj ? 2 : 1);
         }
       }
-      if (ok) umma_commit(o_full);
-      umma_commit(drain);
-      mbar_wait_bounded(drain, 0, kDrainNs, nullptr, 0);
+      if (ok && (NQ == 2 || warp == 2)) umma_commit(o_full);
+      umma_commit(&drain[warp - 1]);
+      mbar_wait_bounded(&drain[warp - 1], 0, kDrainNs, nullptr, 0);
     }
   } else if (warp >= kFirstRowWarp) {
     // ------------------------------ softmax, output ------------------------------
@@ -581,64 +547,80 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
     }
     const float c = p.scale_log2;
     float m = -INFINITY, l = 0.f;  // the maximum that p is relative to, and sum of p
+    // (every lane waits; the warp goes on as one)
+    auto await = [&](uint64_t *bar, uint32_t parity, int site) {
+      return __all_sync(0xffffffffu,
+                        mbar_wait_bounded(bar, parity, p.wait_limit_ns, p.status, site)) != 0;
+    };
+    // With two row tiles their exponentials take turns: the unit that
+    // computes them is then busy with one tile's while the other's scores are
+    // read and its weights written (left alone, both tiles' warps fall into
+    // step and idle it half the time).  Every warp passes every turn, after a
+    // wait that ran out too, so no turn is waited for in vain.
+    auto take_turn = [&]() {
+      if constexpr (NQ == 2) named_barrier_sync(1 + wg, 256);
+    };
+    auto pass_turn = [&](int j) {
+      if constexpr (NQ == 2)
+        if (wg == 0 || j + 1 < nj) named_barrier_arrive(2 - wg, 256);
+    };
+    if (NQ == 2 && wg == 1 && nj > 0) named_barrier_arrive(1, 256);
     for (int j = 0; j < nj; ++j) {
       const int t0 = tiles.at(j0 + j) * KT;
       const bool masked = !every.covers(t0, t0 + KT);
       const int slot = j & 1;
-      if (!mbar_wait_bounded(&s_full[2 * wg + slot], static_cast<uint32_t>(j >> 1) & 1u,
-                             p.wait_limit_ns, p.status, 35)) {
-        ok = false;
-        break;
-      }
-      __syncwarp();
-      tc_fence_after();
       const uint32_t sc = s_col(wg, slot) + lanes;
       uint32_t raw[KT];
-      if constexpr (KT == 128) tmem_ld_all128(sc, raw);
-      else tmem_ld_all64(sc, raw);
-      if (masked) {
+      if (ok) ok = await(&s_full[2 * wg + slot], static_cast<uint32_t>(j >> 1) & 1u, 35);
+      if (ok) {
+        tc_fence_after();
+        if constexpr (KT == 128) tmem_ld_all128(sc, raw);
+        else tmem_ld_all64(sc, raw);
+        if (masked) {
 #pragma unroll
-        for (int i = 0; i < KT; i += 32) {
-          const uint32_t bits = mine.bits(t0 + i);
+          for (int i = 0; i < KT; i += 32) {
+            const uint32_t bits = mine.bits(t0 + i);
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (!(bits >> e & 1u)) raw[i + e] = 0xff800000u;  // -inf
+            for (int e = 0; e < 32; ++e)
+              if (!(bits >> e & 1u)) raw[i + e] = 0xff800000u;  // -inf
+          }
+        }
+        float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < KT; e += 8)
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            top4[u] = max3(top4[u], __uint_as_float(raw[e + 2 * u]), __uint_as_float(raw[e + 2 * u + 1]));
+        const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+        const bool grow = (fmaxf(top, m) - m) * c > kGrow;  // (false for a row that saw nothing)
+        if (__any_sync(0xffffffffu, grow)) {
+          const float m2 = grow ? fmaxf(top, m) : m;
+          const float f = grow ? exp2_fast((m - m2) * c) : 1.f;
+          m = m2;
+          l *= f;
+          if (j > 0) {
+            // (the products of the tile before still add to O)
+            ok = await(&pv_done[2 * wg + ((j - 1) & 1)], static_cast<uint32_t>((j - 1) >> 1) & 1u,
+                       36);
+            tc_fence_after();
+            const uint32_t o = o_col + wg * o_cols + lanes;
+#pragma unroll 1
+            for (uint32_t i = 0; i < o_cols; i += 32) {
+              uint32_t v[32];
+              tmem_ld32_nowait(o + i, v);
+              tmem_wait_ld();
+              tmem_regs_after_wait<32>(v);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+              tmem_st32(o + i, v);
+            }
+          }
         }
       }
-      float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int e = 0; e < KT; e += 8)
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          top4[u] = max3(top4[u], __uint_as_float(raw[e + 2 * u]), __uint_as_float(raw[e + 2 * u + 1]));
-      const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
-      const bool grow = (fmaxf(top, m) - m) * c > kGrow;  // (false for a row that saw nothing)
-      if (__any_sync(0xffffffffu, grow)) {
-        const float m2 = grow ? fmaxf(top, m) : m;
-        const float f = grow ? exp2_fast((m - m2) * c) : 1.f;
-        m = m2;
-        l *= f;
-        if (j > 0) {
-          // (the products of the tile before still add to O)
-          if (!mbar_wait_bounded(&pv_done[wg], static_cast<uint32_t>(j - 1) & 1u, p.wait_limit_ns,
-                                 p.status, 36)) {
-            ok = false;
-            break;
-          }
-          __syncwarp();
-          tc_fence_after();
-          const uint32_t o = o_col + wg * o_cols + lanes;
-#pragma unroll 1
-          for (uint32_t i = 0; i < o_cols; i += 32) {
-            uint32_t v[32];
-            tmem_ld32_nowait(o + i, v);
-            tmem_wait_ld();
-            tmem_regs_after_wait<32>(v);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
-            tmem_st32(o + i, v);
-          }
-        }
+      take_turn();
+      if (!ok) {
+        pass_turn(j);
+        continue;
       }
       const float mc = m == -INFINITY ? 0.f : m * c;
       const uint64_t c2 = pair_of(c, c), mc2 = pair_of(-mc, -mc);
@@ -660,20 +642,18 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
         const float2 x = unpair(pair_add(sum[0], sum[1]));
         l += x.x + x.y;
       }
+      pass_turn(j);
       tmem_wait_st();
-      if (wg == 0 && masked && !any.covers(t0, t0 + KT)) {
+      if (masked && !any.covers(t0, t0 + KT)) {
         // Values no query of the CTA sees may be anything (a slot never
         // written, a frame beyond the end): 0 times a NaN would reach the
-        // sums, so their rows are cleared before the products read them (the
-        // first row tile's come first).
+        // sums, so their rows are cleared before the products read them (by
+        // both row tiles, each before its own products).
         const int pos = ((j + 1 < nj ? j + 2 : nj) + j) * NG;
         for (int g = 0; g < NG; ++g) {
           const int sl = (pos + g) % stages;
-          if (!mbar_wait_bounded(&full[sl], static_cast<uint32_t>((pos + g) / stages) & 1u,
-                                 p.wait_limit_ns, p.status, 37)) {
-            ok = false;
-            break;
-          }
+          ok = await(&full[sl], static_cast<uint32_t>((pos + g) / stages) & 1u, 37);
+          if (!ok) break;
           if (r < KT && !any.has(t0 + r)) {
             uint4 *row =
                 reinterpret_cast<uint4 *>(smem + S::kQ + sl * S::kGroup + r * 128);
@@ -683,7 +663,7 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
                 row[c * (S::kChunk / 16) + e] = make_uint4(0, 0, 0, 0);
           }
         }
-        if (!ok) break;
+        if (!ok) continue;
         fence_proxy_async_smem();
       }
       tc_fence_before();
@@ -691,8 +671,7 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
       if (lane == 0) mbar_arrive(&p_ready[2 * wg + slot]);
     }
     if (nj > 0 && ok) {
-      ok = mbar_wait_bounded(o_full, 0, p.wait_limit_ns, p.status, 38);
-      __syncwarp();
+      ok = await(o_full, 0, 38);
       tc_fence_after();
     }
     if (split == 1 && ok) {

@@ -441,6 +441,11 @@ __device__ __forceinline__ void named_barrier_sync(int id, int count) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
+// Arrive on barrier `id` without waiting for it.
+__device__ __forceinline__ void named_barrier_arrive(int id, int count) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
 // After tmem_wait_ld(): ties each register to a point after the wait, so the
 // compiler cannot move a use of a loaded value above the wait.
 template <int N>
