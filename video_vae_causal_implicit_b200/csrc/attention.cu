@@ -29,6 +29,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 #include <mutex>
 
@@ -134,6 +135,13 @@ struct TileList {
     j -= count[0];
     if (j < count[1]) return start[1] + j;
     return start[2] + (j - count[1]);
+  }
+  // the tile at position j, `tile` being the one before
+  __device__ __forceinline__ int after(int tile, int j) const {
+    ++tile;
+    if (j == count[0]) tile = count[1] > 0 ? start[1] : start[2];
+    else if (j == count[0] + count[1]) tile = start[2];
+    return tile;
   }
 };
 
@@ -550,7 +558,8 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
     // (every lane waits; the warp goes on as one)
     auto await = [&](uint64_t *bar, uint32_t parity, int site) {
       return __all_sync(0xffffffffu,
-                        mbar_wait_bounded(bar, parity, p.wait_limit_ns, p.status, site)) != 0;
+                        mbar_test(bar, parity) ||
+                            mbar_wait_bounded(bar, parity, p.wait_limit_ns, p.status, site)) != 0;
     };
     // With two row tiles their exponentials take turns: the unit that
     // computes them is then busy with one tile's while the other's scores are
@@ -565,8 +574,10 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
         if (wg == 0 || j + 1 < nj) named_barrier_arrive(2 - wg, 256);
     };
     if (NQ == 2 && wg == 1 && nj > 0) named_barrier_arrive(1, 256);
-    for (int j = 0; j < nj; ++j) {
-      const int t0 = tiles.at(j0 + j) * KT;
+    int tile = nj > 0 ? tiles.at(j0) : 0;
+#pragma unroll 1
+    for (int j = 0; j < nj; ++j, tile = tiles.after(tile, j0 + j)) {
+      const int t0 = tile * KT;
       const bool masked = !every.covers(t0, t0 + KT);
       const int slot = j & 1;
       const uint32_t sc = s_col(wg, slot) + lanes;
@@ -846,24 +857,88 @@ __global__ void __launch_bounds__(256)
 using AttnKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap,
                             const AttnArgs);
 
-cudaError_t prepare_kernels() {
-  static std::mutex mu;
-  static bool done[64] = {false};
+// The kernels: head sizes (d_above, d_most] in whole chunks of 64 channels,
+// zero-padded; `step`: cycles of a key tile, measured in the loop.
+struct Variant {
+  AttnKernel kernel;
+  int nq, kt, d_above, d_most, threads;
+  uint32_t smem;
+  double step;
+};
+constexpr int kVariants = 6;
+template <int NQ, int KT, int CH>
+Variant variant(int d_above, double step) {
+  return Variant{attn_kernel<NQ, KT, CH>, NQ, KT, d_above, 64 * CH, attn_threads(NQ),
+                 Shape<NQ, KT, CH>::kSmem, step};
+}
+const Variant (&variants())[kVariants] {
+  static const Variant v[kVariants] = {
+      variant<2, 64, 1>(0, 1600.0),    variant<2, 64, 2>(64, 1700.0), variant<1, 128, 1>(0, 2000.0),
+      variant<1, 128, 2>(64, 2600.0), variant<1, 64, 4>(128, 1800.0), variant<1, 64, 6>(256, 2400.0)};
+  return v;
+}
+
+cudaLaunchConfig_t launch_config(const Variant &v, unsigned grid, int split,
+                                 cudaLaunchAttribute *attr, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  unsigned n = 0;
+  attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  if (split > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = static_cast<unsigned>(split);
+    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(v.threads);
+  cfg.dynamicSmemBytes = v.smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  return cfg;
+}
+
+// Per device: the kernels' shared-memory limit, and how many clusters of 1 to
+// 8 CTAs of each kernel are resident at once.
+struct Prepared {
+  bool done;
+  int fit[kVariants][9];
+};
+std::mutex g_prepare_mu;
+Prepared g_prepared[64];
+
+cudaError_t prepare_kernels(int sm_count, const Prepared **out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  std::lock_guard<std::mutex> lk(mu);
-  if (done[dev]) return cudaSuccess;
-  const AttnKernel ks[6] = {attn_kernel<2, 64, 1>,  attn_kernel<2, 64, 2>, attn_kernel<1, 128, 1>,
-                            attn_kernel<1, 128, 2>, attn_kernel<1, 64, 4>, attn_kernel<1, 64, 6>};
-  for (const AttnKernel k : ks) {
-    e = cudaFuncSetAttribute(reinterpret_cast<const void *>(k),
-                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kSmemMost));
-    if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lk(g_prepare_mu);
+  Prepared &p = g_prepared[dev];
+  if (!p.done) {
+    for (int i = 0; i < kVariants; ++i) {
+      const Variant &v = variants()[i];
+      e = cudaFuncSetAttribute(reinterpret_cast<const void *>(v.kernel),
+                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(v.smem));
+      if (e != cudaSuccess) return e;
+      p.fit[i][1] = sm_count;  // (one CTA per SM)
+      for (int split = 2; split <= 8; ++split) {
+        cudaLaunchAttribute attr[2];
+        const cudaLaunchConfig_t cfg =
+            launch_config(v, static_cast<unsigned>(split), split, attr, nullptr);
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void *>(v.kernel), &cfg) !=
+            cudaSuccess) {
+          (void)cudaGetLastError();
+          n = 0;
+        }
+        p.fit[i][split] = n;
+      }
+    }
+    p.done = true;
   }
-  done[dev] = true;
+  *out = &p;
   return cudaSuccess;
 }
 
@@ -885,7 +960,8 @@ bool encode_heads(CUtensorMap *m, const void *base, int d, int heads, long long 
 cudaError_t launch_attention(AttnArgs a, const void *q, const Strides &sq, const void *k,
                              const Strides &sk, const void *v, const Strides &sv, int sm_count,
                              cudaStream_t stream) {
-  cudaError_t e = prepare_kernels();
+  const Prepared *prepared = nullptr;
+  cudaError_t e = prepare_kernels(sm_count, &prepared);
   if (e != cudaSuccess) return e;
   const CacheShape &c = a.c;
   a.group = a.heads / c.kv_heads;
@@ -910,28 +986,47 @@ cudaError_t launch_attention(AttnArgs a, const void *q, const Strides &sq, const
     *per_frame = 0;
     return across;
   };
-  // Two row tiles a CTA (a key tile read once for both, one's softmax under
-  // the other's products) when that still gives every SM a CTA; their
-  // accumulators fit up to d = 128.
-  int per_frame = 0;
-  const long long tiles1 = tile_count(1, &per_frame);
-  long long q_tiles = tile_count(2, &per_frame);
-  const bool two = c.d <= 128 && q_tiles * heads >= sm_count / 2 && tiles1 > 1;
-  if (!two) q_tiles = tile_count(1, &per_frame);
-  const int nq = two ? 2 : 1;
-  const int kt = (c.d <= 128 && !two) ? 128 : 64;
-  a.q_tiles = static_cast<int>(q_tiles);
-  a.tiles_frame = per_frame;
-  a.split = 1;
-  if (!two) {
-    // keys split over a cluster until every SM has a part of two tiles or more
-    const long long most = (a.window > 0 ? seen + c.t - 1 : seen);
-    const long long keys = (most < c.slots ? most : c.slots) * c.frame;
-    const long long key_tiles = (keys + kt - 1) / kt;
-    while (a.split < 8 && (a.split + 1) * q_tiles * heads <= sm_count &&
-           key_tiles >= 2 * (a.split + 1))
-      ++a.split;
+  const long long have = c.k_frames || c.ring > 0 ? c.slots : c.total;  // frames there are
+  // Candidates: two row tiles a CTA (d <= 128: a key tile is read once for
+  // both, and one's softmax runs under the other's products) or one, keys
+  // split over 1 to 8 CTAs of a cluster; the least time by the cycles that
+  // the steps of a key tile, a CTA's start and end, and the joining of the
+  // parts were measured to take, over whole waves of what fits at once.
+  double best = 1e300;
+  long long q_tiles = 0;
+  const Variant *pick = nullptr;
+  for (const Variant &v : variants()) {
+    if (c.d > v.d_most || c.d <= v.d_above) continue;
+    int per_frame = 0;
+    const long long tiles = tile_count(v.nq, &per_frame);
+    if (tiles * heads > INT32_MAX / 8) continue;
+    // key tiles of a query tile (its first frame's window and what its later
+    // frames add)
+    const long long span =
+        per_frame > 0 ? 1 : (static_cast<long long>(v.nq) * a.tok_tile - 1) / c.frame + 1;
+    const long long frames = seen + (span < c.t ? span : c.t) - 1;
+    const long long keys = (frames < have ? frames : have) * c.frame;
+    const double steps = static_cast<double>((keys + v.kt - 1) / v.kt);
+    for (int split = 1; split <= 8 && (split == 1 || split * 2 <= steps); ++split) {
+      const int fit = prepared->fit[&v - variants()][split];
+      if (fit < 1) continue;
+      // (a few waves are whole ones; the last of many overlaps the others')
+      const double parts = static_cast<double>(tiles * heads) / fit;
+      const double waves = parts < 4.0 ? std::ceil(parts) : parts + 0.5;
+      const double t = waves * (std::ceil(steps / split) * v.step + 7000.0 +
+                                (split > 1 ? 3000.0 + 8.0 * v.nq * c.d : 0.0));
+      if (t < best) {
+        best = t;
+        pick = &v;
+        q_tiles = tiles;
+        a.split = split;
+        a.tiles_frame = per_frame;
+      }
+    }
   }
+  if (!pick) return cudaErrorInvalidValue;
+  const int kt = pick->kt;
+  a.q_tiles = static_cast<int>(q_tiles);
   const long long grid = q_tiles * heads * a.split;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
   CUtensorMap mq, mk, mv;
@@ -940,31 +1035,10 @@ cudaError_t launch_attention(AttnArgs a, const void *q, const Strides &sq, const
       !encode_heads(&mk, k, c.d, c.kv_heads, cached, c.n, sk, 1, kt) ||
       !encode_heads(&mv, v, c.d, c.kv_heads, cached, c.n, sv, 1, kt))
     return cudaErrorInvalidValue;
-  // (channels are padded with zeros to whole chunks of the kernel's shape)
-  AttnKernel kern;
-  uint32_t smem;
-#define CC3D_ATTN(...) (kern = attn_kernel<__VA_ARGS__>, smem = Shape<__VA_ARGS__>::kSmem)
-  if (two && c.d <= 64) CC3D_ATTN(2, 64, 1);
-  else if (two) CC3D_ATTN(2, 64, 2);
-  else if (c.d <= 64) CC3D_ATTN(1, 128, 1);
-  else if (c.d <= 128) CC3D_ATTN(1, 128, 2);
-  else if (c.d <= 256) CC3D_ATTN(1, 64, 4);
-  else CC3D_ATTN(1, 64, 6);
-#undef CC3D_ATTN
-  cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(a.split);
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(attn_threads(nq));
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = a.split > 1 ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, static_cast<const AttnArgs>(a));
+  const cudaLaunchConfig_t cfg =
+      launch_config(*pick, static_cast<unsigned>(grid), a.split, attr, stream);
+  e = cudaLaunchKernelEx(&cfg, pick->kernel, mq, mk, mv, static_cast<const AttnArgs>(a));
   count_launch();
   return e;
 }
