@@ -349,43 +349,64 @@ def quantize_e4m3(x, scale, q, stream=None):
 # ---- transformer operators ---------------------------------------------------------
 #
 # The C calls see addresses only, so these wrappers check what the addresses
-# stand for: type, device (the current one), shape and strides.
+# stand for: type, device (the current one), shape and strides.  A small call
+# takes as long as its checks, so each is one expression and the reasons are
+# worked out only for a tensor that fails it.
 
-def _arg(t, name, dtypes, device, shape=None, rows=False):
-    """The address of `t` (None stays None), checked.  rows: the last
-    dimension is contiguous, the one before it may be strided; else the
-    tensor is contiguous."""
-    if t is None:
-        return None
+_torch = None  # torch and the types of the operators, on first use
+_B16 = _F32 = _B8 = _I32 = ()
+
+
+def _load_torch():
+    global _torch, _B16, _F32, _B8, _I32
+    import torch
+    _B16, _F32, _I32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
+    _B8 = (torch.float8_e4m3fn, torch.uint8)
+    _torch = torch
+
+
+def _current(t, name, stream):
+    """(device index, raw stream) of a call whose first tensor is `t`."""
+    if _torch is None:
+        _load_torch()
+    dev = t.get_device()
+    if dev < 0 or dev != _torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
+    if stream is None:
+        return dev, _torch._C._cuda_getCurrentRawStream(dev)
+    return dev, stream.cuda_stream
+
+
+def _refuse(t, name, dtypes, dev, shape):
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: {t.dtype}, expected {' or '.join(map(str, dtypes))}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if rows:
-        if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-            raise ValueError(f"{name}: a matrix with contiguous rows is expected")
-    elif not t.is_contiguous():
-        raise ValueError(f"{name}: not contiguous")
+    raise ValueError(f"{name}: strides {t.stride()} of shape {tuple(t.shape)}; contiguous "
+                     "elements (or rows, where rows may be strided) expected")
+
+
+def _flat(t, name, dtypes, dev, shape):
+    """The address of a contiguous tensor, checked (None: 0)."""
+    if t is None:
+        return 0
+    if (t.dtype not in dtypes or t.get_device() != dev or t.shape != shape
+            or not t.is_contiguous()):
+        _refuse(t, name, dtypes, dev, shape)
     return t.data_ptr()
 
 
-def _device(t, name):
-    import torch
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
-    return t.device
-
-
-def _row_step(t):
+def _rows(t, name, dtypes, dev, shape):
+    """(address, distance of rows) of a matrix with contiguous rows, checked."""
+    if t.dtype not in dtypes or t.get_device() != dev or t.shape != shape or len(shape) != 2:
+        _refuse(t, name, dtypes, dev, shape)
+    step, one = t.stride()
+    if one != 1 and shape[1] > 1:
+        _refuse(t, name, dtypes, dev, shape)
     # (the distance of a single row is free: any legal one will do)
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
-
-
-def _types():
-    import torch
-    return (torch.bfloat16,), (torch.float32,), (torch.float8_e4m3fn, torch.uint8)
+    return t.data_ptr(), step if shape[0] > 1 else shape[1]
 
 
 def linear(x, weight, y, *, bias=None, residual=None, act=ACT_NONE, x_scales=None, w_scales=None,
@@ -395,23 +416,21 @@ def linear(x, weight, y, *, bias=None, residual=None, act=ACT_NONE, x_scales=Non
     x [m, k] and weight [n, k] are bf16, or both E4M3 codes (float8_e4m3fn or
     uint8) with w_scales [n] and x_scales [m] (or one x_scale); bias fp32 [n];
     residual and y bf16 [m, n] (y may be the residual).  Rows may be strided."""
-    b16, f32, b8 = _types()
-    dev = _device(x, "x")
-    fp8 = x.dtype in b8
-    ops = b8 if fp8 else b16
-    px = _arg(x, "x", ops, dev, rows=True)
+    dev, st = _current(x, "x", stream)
+    fp8 = x.dtype in _B8
+    ops = _B8 if fp8 else _B16
+    if x.dim() != 2 or weight.dim() != 2:
+        raise ValueError("x [m, k] and weight [n, k] expected")
     m, k = x.shape
-    pw = _arg(weight, "weight", ops, dev, rows=True)
     n = weight.shape[0]
-    if weight.shape[1] != k:
-        raise ValueError(f"weight: {weight.shape[1]} columns, x has {k}")
-    py = _arg(y, "y", b16, dev, (m, n), rows=True)
-    pr = _arg(residual, "residual", b16, dev, (m, n), rows=True)
-    check(lib().cc3d_linear(
-        px, _row_step(x), pw, _row_step(weight), _arg(bias, "bias", f32, dev, (n,)), pr,
-        _row_step(residual) if residual is not None else 0, py, _row_step(y), m, n, k,
-        FP8_E4M3 if fp8 else BF16, act, _arg(x_scales, "x_scales", f32, dev, (m,)), x_scale,
-        _arg(w_scales, "w_scales", f32, dev, (n,)), _stream(stream)), "cc3d_linear")
+    px, ldx = _rows(x, "x", ops, dev, x.shape)
+    pw, ldw = _rows(weight, "weight", ops, dev, (n, k))
+    py, ldy = _rows(y, "y", _B16, dev, (m, n))
+    pr, ldr = _rows(residual, "residual", _B16, dev, (m, n)) if residual is not None else (0, 0)
+    check((_lib or lib()).cc3d_linear(
+        px, ldx, pw, ldw, _flat(bias, "bias", _F32, dev, (n,)), pr, ldr, py, ldy, m, n, k,
+        FP8_E4M3 if fp8 else BF16, act, _flat(x_scales, "x_scales", _F32, dev, (m,)), x_scale,
+        _flat(w_scales, "w_scales", _F32, dev, (n,)), st), "cc3d_linear")
     return y
 
 
@@ -421,17 +440,16 @@ def add_rms_norm(x, gamma, *, residual=None, beta=None, eps=0.0, silu=False, h=N
     16 bits (y), in E4M3 (q, with row scales written to `scales` or one given
     `scale`), and the sum itself (h); see cc3d_add_rms_norm.  Outputs are the
     tensors given; returns None."""
-    b16, f32, b8 = _types()
-    dev = _device(x, "x")
-    c = x.shape[-1]
-    rows = x.numel() // c if c else 0
+    dev, st = _current(x, "x", stream)
     shape = x.shape
-    check(lib().cc3d_add_rms_norm(
-        _arg(x, "x", b16, dev), _arg(residual, "residual", b16, dev, shape),
-        _arg(gamma, "gamma", f32, dev, (c,)), _arg(beta, "beta", f32, dev, (c,)), rows, c, eps,
-        1 if silu else 0, _arg(h, "h", b16, dev, shape), _arg(y, "y", b16, dev, shape),
-        _arg(q, "q", b8, dev, shape), _arg(scales, "scales", f32, dev, shape[:-1]), scale,
-        _stream(stream)), "cc3d_add_rms_norm")
+    c = shape[-1]
+    rows = x.numel() // c if c else 0
+    check((_lib or lib()).cc3d_add_rms_norm(
+        _flat(x, "x", _B16, dev, shape), _flat(residual, "residual", _B16, dev, shape),
+        _flat(gamma, "gamma", _F32, dev, (c,)), _flat(beta, "beta", _F32, dev, (c,)), rows, c, eps,
+        1 if silu else 0, _flat(h, "h", _B16, dev, shape), _flat(y, "y", _B16, dev, shape),
+        _flat(q, "q", _B8, dev, shape), _flat(scales, "scales", _F32, dev, shape[:-1]), scale,
+        st), "cc3d_add_rms_norm")
 
 
 # cc3d_attn_call and cc3d_kv_call as the C compiler lays them out
@@ -439,29 +457,29 @@ _ATTN_CALL = struct.Struct("@11if6P12q")
 _KV_CALL = struct.Struct("@9i6P12q")
 
 
-def _heads(t, name, b16, dev, frames_of=None):
-    """The address of a [n, tokens, heads, d] bf16 tensor with a contiguous
-    last dimension, checked."""
-    if t.dtype not in b16:
-        raise TypeError(f"{name}: {t.dtype}, expected torch.bfloat16")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if t.dim() != 4 or (t.shape[3] > 1 and t.stride(3) != 1):
-        raise ValueError(f"{name}: [n, tokens, heads, d] with a contiguous last dimension expected")
-    if frames_of is not None and t.shape[1] % frames_of:
-        raise ValueError(f"{name}: {t.shape[1]} tokens are not whole frames of {frames_of}")
-    return t.data_ptr()
+def _heads(t, name, dev, shape, frame):
+    """(address, strides of sequences, tokens and heads) of a [n, tokens,
+    heads, d] bf16 tensor with a contiguous last dimension, checked."""
+    if t.dtype not in _B16 or t.get_device() != dev or t.shape != shape or len(shape) != 4:
+        _refuse(t, name, _B16, dev, shape)
+    a, b, c, one = t.stride()
+    if (one != 1 and shape[3] > 1) or shape[1] % frame:
+        if shape[1] % frame == 0:
+            _refuse(t, name, _B16, dev, shape)
+        raise ValueError(f"{name}: {shape[1]} tokens are not whole frames of {frame}")
+    return t.data_ptr(), a, b, c
 
 
-def _lengths(n, frame, sinks, ring, total, q_frames, k_frames, dev):
-    import torch
+def _lengths(n, frame, total, q_frames, k_frames, dev):
     if frame < 1:
         raise ValueError(f"frame: {frame}")
-    i32 = (torch.int32,)
-    if k_frames is None and total is None:
-        raise ValueError("total or k_frames is needed")
-    return (_arg(q_frames, "q_frames", i32, dev, (n,)) or 0,
-            _arg(k_frames, "k_frames", i32, dev, (n,)) or 0, 0 if total is None else total)
+    if k_frames is None:
+        if total is None:
+            raise ValueError("total or k_frames is needed")
+    elif total is None:
+        total = 0
+    return (total, _flat(q_frames, "q_frames", _I32, dev, (n,)),
+            _flat(k_frames, "k_frames", _I32, dev, (n,)))
 
 
 def attention(q, k, v, o, *, frame=1, window=0, sinks=0, ring=0, total=None, q_frames=None,
@@ -471,20 +489,21 @@ def attention(q, k, v, o, *, frame=1, window=0, sinks=0, ring=0, total=None, q_f
     [n, slots * frame, kv_heads, d], bf16, any strides with a contiguous last
     dimension.  total: frames of every sequence, this chunk included, or
     k_frames (int32 [n], device) one count each; window 0: unlimited."""
-    b16, _, _ = _types()
-    dev = _device(q, "q")
-    n, qt, heads, d = q.shape if q.dim() == 4 else (0, 0, 0, 0)
-    pq_, pk_, total = _lengths(n, frame, sinks, ring, total, q_frames, k_frames, dev)
-    pq, pk = _heads(q, "q", b16, dev, frame), _heads(k, "k", b16, dev, frame)
-    pv, po = _heads(v, "v", b16, dev, frame), _heads(o, "o", b16, dev, frame)
-    kv = k.shape
-    if kv[0] != n or kv[3] != d or v.shape != kv or o.shape != q.shape:
-        raise ValueError(f"q {tuple(q.shape)}, k {tuple(kv)}, v {tuple(v.shape)}, "
-                         f"o {tuple(o.shape)} do not fit")
-    call = _ATTN_CALL.pack(n, heads, kv[2], d, frame, qt // frame, kv[1] // frame, window, sinks,
-                           ring, total, scale, pq_, pk_, pq, pk, pv, po, *q.stride()[:3],
-                           *k.stride()[:3], *v.stride()[:3], *o.stride()[:3])
-    check(lib().cc3d_attention(call, _stream(stream)), "cc3d_attention")
+    dev, st = _current(q, "q", stream)
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q [n, tokens, heads, d] and k [n, tokens, kv_heads, d] expected")
+    n, qt, heads, d = q.shape
+    _, kt, kv_heads, _ = k.shape
+    total, pqf, pkf = _lengths(n, frame, total, q_frames, k_frames, dev)
+    cache = (n, kt, kv_heads, d)
+    pq, q0, q1, q2 = _heads(q, "q", dev, q.shape, frame)
+    pk, k0, k1, k2 = _heads(k, "k", dev, cache, frame)
+    pv, v0, v1, v2 = _heads(v, "v", dev, cache, frame)
+    po, o0, o1, o2 = _heads(o, "o", dev, q.shape, frame)
+    check((_lib or lib()).cc3d_attention(
+        _ATTN_CALL.pack(n, heads, kv_heads, d, frame, qt // frame, kt // frame, window, sinks,
+                        ring, total, scale, pqf, pkf, pq, pk, pv, po, q0, q1, q2, k0, k1, k2, v0,
+                        v1, v2, o0, o1, o2), st), "cc3d_attention")
     return o
 
 
@@ -493,21 +512,21 @@ def kv_append(k, v, k_cache, v_cache, *, frame=1, sinks=0, ring=0, total=None, q
     """A chunk's keys and values [n, t * frame, kv_heads, d] into the caches
     [n, slots * frame, kv_heads, d] (cc3d_kv_append); frame counts as in
     attention, the chunk included."""
-    b16, _, _ = _types()
-    dev = _device(k, "k")
-    n, kt, heads, d = k.shape if k.dim() == 4 else (0, 0, 0, 0)
-    pq_, pk_, total = _lengths(n, frame, sinks, ring, total, q_frames, k_frames, dev)
-    pk, pv = _heads(k, "k", b16, dev, frame), _heads(v, "v", b16, dev, frame)
-    pkc = _heads(k_cache, "k_cache", b16, dev, frame)
-    pvc = _heads(v_cache, "v_cache", b16, dev, frame)
-    cs = k_cache.shape
-    if v.shape != k.shape or v_cache.shape != cs or cs[0] != n or tuple(cs[2:]) != (heads, d):
-        raise ValueError(f"k {tuple(k.shape)}, v {tuple(v.shape)}, k_cache {tuple(cs)}, "
-                         f"v_cache {tuple(v_cache.shape)} do not fit")
-    call = _KV_CALL.pack(n, heads, d, frame, kt // frame, cs[1] // frame, sinks, ring, total, pq_,
-                         pk_, pk, pv, pkc, pvc, *k.stride()[:3], *v.stride()[:3],
-                         *k_cache.stride()[:3], *v_cache.stride()[:3])
-    check(lib().cc3d_kv_append(call, _stream(stream)), "cc3d_kv_append")
+    dev, st = _current(k, "k", stream)
+    if k.dim() != 4 or k_cache.dim() != 4:
+        raise ValueError("k and k_cache [n, tokens, kv_heads, d] expected")
+    n, kt, heads, d = k.shape
+    ct = k_cache.shape[1]
+    total, pqf, pkf = _lengths(n, frame, total, q_frames, k_frames, dev)
+    cache = (n, ct, heads, d)
+    pk, k0, k1, k2 = _heads(k, "k", dev, k.shape, frame)
+    pv, v0, v1, v2 = _heads(v, "v", dev, k.shape, frame)
+    pkc, kc0, kc1, kc2 = _heads(k_cache, "k_cache", dev, cache, frame)
+    pvc, vc0, vc1, vc2 = _heads(v_cache, "v_cache", dev, cache, frame)
+    check((_lib or lib()).cc3d_kv_append(
+        _KV_CALL.pack(n, heads, d, frame, kt // frame, ct // frame, sinks, ring, total, pqf, pkf,
+                      pk, pv, pkc, pvc, k0, k1, k2, v0, v1, v2, kc0, kc1, kc2, vc0, vc1, vc2),
+        st), "cc3d_kv_append")
 
 
 def sync_status(stream=None):
