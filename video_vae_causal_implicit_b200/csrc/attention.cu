@@ -952,7 +952,7 @@ bool encode_heads(CUtensorMap *m, const void *base, int d, int heads, long long 
                                static_cast<uint64_t>(n > 1 ? s.seq : 8) * 2};
   const uint32_t box[4] = {64, static_cast<uint32_t>(box_heads), static_cast<uint32_t>(box_tokens),
                            1};
-  return encode_sw128_map(m, base, 2, 4, dims, strides, box);
+  return encode_rows_map(m, base, 2, 4, dims, strides, box);
 }
 
 }  // namespace

@@ -57,14 +57,25 @@ __device__ __forceinline__ void activate(float (&v)[N], int act) {
   }
 }
 
+// Columns of y that an epilogue warp finishes at a time: rows of 64 bytes in
+// its own part of shared memory, from where TMA stores them (and where it puts
+// the residual's).  (A thread holds a row, so its own stores would touch 32
+// lines at a time; 128-byte rows would cost the ring a stage.)
+constexpr int kOutCols = 32;
+constexpr uint32_t kOutBuf = 32u * kOutCols * 2u;
+
 struct Layout {
-  uint32_t stage, bars, total;  // bytes
+  uint32_t stage, out, params, bars, total;  // bytes
 };
-__host__ __device__ inline Layout ring_layout(int b_rows, int stages) {
+// The ring of operand chunks, and for the many-row kernel the epilogue warps'
+// two output buffers and column parameters (bias and scale).
+__host__ __device__ inline Layout ring_layout(int b_rows, int stages, int nt = 0) {
   Layout l;
   l.stage = kAStage + static_cast<uint32_t>(b_rows) * kRowBytes;
-  l.bars = l.stage * static_cast<uint32_t>(stages);
-  l.total = l.bars + 8u * (2u * stages + 5u) + 16u;
+  l.out = l.stage * static_cast<uint32_t>(stages);
+  l.params = l.out + (nt ? 2u * kEpiWarps * kOutBuf : 0u);
+  l.bars = l.params + (nt ? kEpiWarps * (nt / 2) * 8u : 0u);
+  l.total = l.bars + 8u * (2u * stages + 5u + 2u * kEpiWarps) + 16u;
   return l;
 }
 
@@ -85,18 +96,21 @@ struct TileWalk {
 template <bool FP8, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_kernel(const __grid_constant__ CUtensorMap map_x,
-                  const __grid_constant__ CUtensorMap map_w, const LinearArgs p) {
+                  const __grid_constant__ CUtensorMap map_w,
+                  const __grid_constant__ CUtensorMap map_y,
+                  const __grid_constant__ CUtensorMap map_r, const LinearArgs p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int b_rows = PAIR ? p.nt / 2 : p.nt;  // weight rows this CTA loads
-  const Layout L = ring_layout(b_rows, p.stages);
+  const Layout L = ring_layout(b_rows, p.stages, p.nt);
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + L.bars);
   uint64_t *empty = full + p.stages;
   uint64_t *acc_full = empty + p.stages;  // [2]
   uint64_t *acc_empty = acc_full + 2;     // [2]
   uint64_t *drain = acc_empty + 2;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+  uint64_t *res_full = drain + 1;  // [epilogue warp][2]
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(res_full + 2 * kEpiWarps);
 
   const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
   const int cid = PAIR ? blockIdx.x / 2 : blockIdx.x;
@@ -120,9 +134,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&acc_empty[i], PAIR ? 2 * kEpiWarps : kEpiWarps);
     }
     mbar_init(drain, 1);
+    for (int i = 0; i < 2 * kEpiWarps; ++i) mbar_init(&res_full[i], 1);
     fence_mbar_init();
     prefetch_tmap(&map_x);
     prefetch_tmap(&map_w);
+    prefetch_tmap(&map_y);
   }
   if (warp == 1) {
     if constexpr (PAIR) {
@@ -230,43 +246,76 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait_bounded(drain, 0, kDrainNs, nullptr, 0);
     }
   } else {
-    const int q = warp % 4;              // tensor-memory lanes this warp may read
-    const int half = (warp - 2) / 4;     // its half of the tile's columns
+    const int q = warp % 4;           // tensor-memory lanes this warp may read
+    const int half = (warp - 2) / 4;  // its half of the tile's columns
     const int cols = p.nt / 2;
+    uint8_t *out = smem + L.out + (warp - 2) * 2u * kOutBuf;
+    float *s_bias = reinterpret_cast<float *>(smem + L.params) + (warp - 2) * 2 * cols;
+    float *s_scale = s_bias + cols;
+    uint64_t *res = res_full + 2 * (warp - 2);
     const uint32_t free_bar = PAIR ? mapa_shared(smem_u32(acc_empty), 0u) : 0u;
+    // 16-byte piece i of this thread's row, where the 64-byte swizzle puts it
+    auto piece = [&](int buf, int i) {
+      return reinterpret_cast<uint4 *>(out + buf * kOutBuf + lane * 64u +
+                                       ((static_cast<uint32_t>(i) ^ ((lane >> 1) & 3u)) << 4));
+    };
     griddep_wait();
-    int it = 0;
-    for (int t = cid; t < n_tiles; t += ncl, ++it) {
+    int it = 0, ob = 0;      // tiles, and output buffers used so far
+    uint32_t res_par = 0;    // phase parity of the two residual barriers
+    auto row0_of = [&](int mt) { return mt * kRowsPerTile + rank * kTileRows + q * 32; };
+    // the residual of one buffer's worth of tile t on its way (lane 0): the
+    // buffer's last store has been read
+    auto fetch_residual = [&](int t, int u, int buf) {
       int mt, nt;
       walk.at(t, mt, nt);
-      const int row = mt * kRowsPerTile + rank * kTileRows + q * 32 + lane;
-      const bool live = row < p.m;
+      bulk_groups_wait_read<0>();
+      mbar_arrive_expect_tx(&res[buf], kOutBuf);
+      tma_load_2d(smem_u32(out) + buf * kOutBuf, &map_r, &res[buf],
+                  nt * p.nt + half * cols + u * kOutCols, row0_of(mt));
+    };
+    if (p.residual && lane == 0 && cid < n_tiles) fetch_residual(cid, 0, 0);
+    for (int t = cid; t < n_tiles && ok; t += ncl, ++it) {
+      int mt, nt;
+      walk.at(t, mt, nt);
+      const int row = row0_of(mt) + lane;
       const int n0 = nt * p.nt + half * cols;
-      const int n1 = min(n0 + cols, p.n);  // (may be <= n0: nothing to store)
-      __nv_bfloat16 *yr = p.y + static_cast<long long>(row) * p.ldy;
-      const __nv_bfloat16 *rr =
-          p.residual ? p.residual + static_cast<long long>(row) * p.ldr : nullptr;
-      // the residual's rows into L2 while the MMAs run
-      if (rr && live && n1 > n0) bulk_prefetch_l2(rr + n0, static_cast<uint32_t>(n1 - n0) * 2u);
-      const float xs = FP8 && live ? (p.x_scales ? p.x_scales[row] : p.x_scale) : 1.f;
+      // the columns' parameters, while the MMAs run
+      __syncwarp();
+      for (int i = lane; i < cols; i += 32) {
+        const int c = n0 + i;
+        s_bias[i] = p.bias && c < p.n ? p.bias[c] : 0.f;
+        if constexpr (FP8) s_scale[i] = c < p.n ? p.w_scales[c] : 0.f;
+      }
+      __syncwarp();
+      const float xs = FP8 && row < p.m ? (p.x_scales ? p.x_scales[row] : p.x_scale) : 1.f;
       const int buf = it & 1;
       const uint32_t up = static_cast<uint32_t>((it >> 1) & 1);
-      uint32_t got = 0;
-      if (lane == 0)
-        got = mbar_wait_bounded(&acc_full[buf], up, p.wait_limit_ns, p.status, 23) ? 1u : 0u;
-      got = __shfl_sync(0xffffffffu, got, 0);
-      if (!got) break;
+      ok = __all_sync(0xffffffffu,
+                      mbar_wait_bounded(&acc_full[buf], up, p.wait_limit_ns, p.status, 23));
+      if (!ok) break;
       tc_fence_after();
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                              static_cast<uint32_t>(buf * p.nt + half * cols);
-      for (int j = 0; j < cols; j += 32) {
-        __syncwarp();
+      for (int u = 0; u < cols / kOutCols; ++u, ob ^= 1) {
+        if (p.residual) {
+          // the next buffer's worth (of this tile or the next one) on its way
+          if (lane == 0) {
+            if ((u + 1) * kOutCols < cols) fetch_residual(t, u + 1, ob ^ 1);
+            else if (t + ncl < n_tiles) fetch_residual(t + ncl, 0, ob ^ 1);
+          }
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&res[ob], (res_par >> ob) & 1u,
+                                                         p.wait_limit_ns, p.status, 27));
+          res_par ^= 1u << ob;
+          if (!ok) break;
+        } else {
+          if (lane == 0) bulk_groups_wait_read<1>();
+          __syncwarp();
+        }
         uint32_t raw[32];
-        tmem_ld16_nowait(taddr + j, raw);
-        tmem_ld16_nowait(taddr + j + 16, raw + 16);
+        tmem_ld32_nowait(taddr + u * kOutCols, raw);
         tmem_wait_ld();
         tmem_regs_after_wait<32>(raw);
-        if (j + 32 == cols) {
+        if ((u + 1) * kOutCols == cols) {
           // the accumulator is in registers: the next tile's MMAs may start
           tc_fence_before();
           __syncwarp();
@@ -275,30 +324,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             else mbar_arrive(&acc_empty[buf]);
           }
         }
+        const float *bias = s_bias + u * kOutCols, *scale = s_scale + u * kOutCols;
 #pragma unroll
-        for (int g = 0; g < 32; g += 8) {
-          const int c = n0 + j + g;
-          if (c >= n1 || !live) continue;
+        for (int g = 0; g < kOutCols; g += 8) {
           float v[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(raw[g + e]);
+          const float4 b0 = *reinterpret_cast<const float4 *>(bias + g);
+          const float4 b1 = *reinterpret_cast<const float4 *>(bias + g + 4);
+          const float bs[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
           if constexpr (FP8) {
-            const float4 s0 = *reinterpret_cast<const float4 *>(p.w_scales + c);
-            const float4 s1 = *reinterpret_cast<const float4 *>(p.w_scales + c + 4);
+            const float4 s0 = *reinterpret_cast<const float4 *>(scale + g);
+            const float4 s1 = *reinterpret_cast<const float4 *>(scale + g + 4);
             const float ws[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] *= xs * ws[e];
-          }
-          if (p.bias) {
-            const float4 s0 = *reinterpret_cast<const float4 *>(p.bias + c);
-            const float4 s1 = *reinterpret_cast<const float4 *>(p.bias + c + 4);
-            const float bs[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+            for (int e = 0; e < 8; ++e)
+              v[e] = fmaf(__uint_as_float(raw[g + e]), xs * ws[e], bs[e]);
+          } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] += bs[e];
+            for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(raw[g + e]) + bs[e];
           }
           activate(v, p.act);
-          if (rr) {
-            const uint4 r4 = *reinterpret_cast<const uint4 *>(rr + c);
+          uint4 *at = piece(ob, g / 8);
+          if (p.residual) {
+            const uint4 r4 = *at;
             const uint32_t rw[4] = {r4.x, r4.y, r4.z, r4.w};
 #pragma unroll
             for (int e = 0; e < 8; ++e)
@@ -309,10 +356,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           o.y = pack_bf16x2(v[2], v[3]);
           o.z = pack_bf16x2(v[4], v[5]);
           o.w = pack_bf16x2(v[6], v[7]);
-          *reinterpret_cast<uint4 *>(yr + c) = o;
+          *at = o;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(&map_y, smem_u32(out) + ob * kOutBuf, n0 + u * kOutCols, row0_of(mt));
+          bulk_group_commit();
         }
       }
     }
+    if (lane == 0) {
+      // nothing of this warp's is under way when the CTA ends (a residual
+      // fetch neither after a wait that ran out)
+      bulk_groups_wait();
+      if (!ok && p.residual)
+        for (int i = 0; i < 2; ++i)
+          mbar_wait_bounded(&res[i], (res_par >> i) & 1u, kDrainNs, nullptr, 0);
+    }
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
@@ -567,13 +629,16 @@ Choice choose(const LinearArgs &a, bool fp8, int sm_count) {
       --best.stages;
   } else {
     best.stages = 8;
-    while (ring_layout(best.pair ? best.nt / 2 : best.nt, best.stages).total + 1024 > kSmemMost)
+    while (ring_layout(best.pair ? best.nt / 2 : best.nt, best.stages, best.nt).total + 1024 >
+           kSmemMost)
       --best.stages;
   }
   return best;
 }
 
-using LinearKernel = void (*)(const CUtensorMap, const CUtensorMap, const LinearArgs);
+using LinearKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap,
+                              const CUtensorMap, const LinearArgs);
+using SplitKernel = void (*)(const CUtensorMap, const CUtensorMap, const LinearArgs);
 
 // Pairs of CTAs that can be resident at once, per device (grid of the
 // persistent pair kernel).
@@ -617,11 +682,14 @@ cudaError_t prepare_kernels() {
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lk(mu);
   if (done[dev]) return cudaSuccess;
-  const LinearKernel ks[6] = {linear_kernel<false, false>, linear_kernel<false, true>,
-                              linear_kernel<true, false>,  linear_kernel<true, true>,
-                              linear_split_kernel<false>,  linear_split_kernel<true>};
-  for (const LinearKernel k : ks) {
-    e = cudaFuncSetAttribute(reinterpret_cast<const void *>(k),
+  const void *ks[6] = {reinterpret_cast<const void *>(&linear_kernel<false, false>),
+                       reinterpret_cast<const void *>(&linear_kernel<false, true>),
+                       reinterpret_cast<const void *>(&linear_kernel<true, false>),
+                       reinterpret_cast<const void *>(&linear_kernel<true, true>),
+                       reinterpret_cast<const void *>(&linear_split_kernel<false>),
+                       reinterpret_cast<const void *>(&linear_split_kernel<true>)};
+  for (const void *k : ks) {
+    e = cudaFuncSetAttribute(k,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kSmemMost));
     if (e != cudaSuccess) return e;
@@ -650,7 +718,7 @@ cudaError_t launch_linear(LinearArgs a, const void *x, long long ldx, const void
   const uint64_t sx[1] = {static_cast<uint64_t>(ldx) * esz};
   const uint64_t sw[1] = {static_cast<uint64_t>(ldw) * esz};
   const uint32_t bx[2] = {chunk, x_rows}, bw[2] = {chunk, w_rows};
-  if (!encode_sw128_map(&mx, x, esz, 2, dx, sx, bx) || !encode_sw128_map(&mw, w, esz, 2, dw, sw, bw))
+  if (!encode_rows_map(&mx, x, esz, 2, dx, sx, bx) || !encode_rows_map(&mw, w, esz, 2, dw, sw, bw))
     return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
@@ -658,17 +726,29 @@ cudaError_t launch_linear(LinearArgs a, const void *x, long long ldx, const void
   attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[na].val.programmaticStreamSerializationAllowed = 1;
   ++na;
-  LinearKernel k;
+  LinearKernel k = nullptr;
+  SplitKernel ks = nullptr;
   unsigned cluster = 1;
+  CUtensorMap my, mr;
+  if (!c.split_kernel) {
+    const uint64_t dy[2] = {static_cast<uint64_t>(a.n), static_cast<uint64_t>(a.m)};
+    const uint64_t sy[1] = {static_cast<uint64_t>(a.ldy) * 2};
+    const uint64_t sr[1] = {static_cast<uint64_t>(a.ldr) * 2};
+    const uint32_t by[2] = {kOutCols, 32};
+    if (!encode_rows_map(&my, a.y, 2, 2, dy, sy, by)) return cudaErrorInvalidValue;
+    mr = my;
+    if (a.residual && !encode_rows_map(&mr, a.residual, 2, 2, dy, sr, by))
+      return cudaErrorInvalidValue;
+  }
   if (c.split_kernel) {
-    k = fp8 ? linear_split_kernel<true> : linear_split_kernel<false>;
+    ks = fp8 ? linear_split_kernel<true> : linear_split_kernel<false>;
     const unsigned tiles = static_cast<unsigned>(((a.n + 127) / 128) * ((a.m + c.nt - 1) / c.nt));
     cfg.gridDim = dim3(tiles * c.split);
     cfg.blockDim = dim3(kSplitThreads);
     cfg.dynamicSmemBytes = split_total(c.nt, c.stages) + 1024;
     cluster = c.split;
   } else {
-    const size_t smem = ring_layout(c.pair ? c.nt / 2 : c.nt, c.stages).total + 1024;
+    const size_t smem = ring_layout(c.pair ? c.nt / 2 : c.nt, c.stages, c.nt).total + 1024;
     const int rows = c.pair ? 256 : 128;
     const long long tiles =
         static_cast<long long>((a.m + rows - 1) / rows) * ((a.n + c.nt - 1) / c.nt);
@@ -695,7 +775,9 @@ cudaError_t launch_linear(LinearArgs a, const void *x, long long ldx, const void
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = na;
-  e = cudaLaunchKernelEx(&cfg, k, mx, mw, static_cast<const LinearArgs>(a));
+  const LinearArgs args = a;
+  e = ks ? cudaLaunchKernelEx(&cfg, ks, mx, mw, args)
+         : cudaLaunchKernelEx(&cfg, k, mx, mw, my, mr, args);
   count_launch();
   return e;
 }

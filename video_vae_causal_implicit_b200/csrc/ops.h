@@ -35,9 +35,9 @@ struct DeviceInfo {
 bool device_info(DeviceInfo *out);
 
 // A tiled tensor map with `rank` dimensions of bf16 (esz 2) or byte (esz 1)
-// elements, the 128-byte swizzle and zero fill out of bounds.  strides: bytes
-// of dimensions 1 .. rank - 1.
-bool encode_sw128_map(CUtensorMap *m, const void *base, int esz, int rank, const uint64_t *dims,
+// elements, boxes of 128- or 64-byte rows with the swizzle of that length, and
+// zero fill out of bounds.  strides: bytes of dimensions 1 .. rank - 1.
+bool encode_rows_map(CUtensorMap *m, const void *base, int esz, int rank, const uint64_t *dims,
                       const uint64_t *strides, const uint32_t *box);
 
 struct AddNormArgs {

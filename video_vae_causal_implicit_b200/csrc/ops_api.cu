@@ -38,7 +38,7 @@ bool device_info(DeviceInfo *out) {
   return true;
 }
 
-bool encode_sw128_map(CUtensorMap *m, const void *base, int esz, int rank, const uint64_t *dims,
+bool encode_rows_map(CUtensorMap *m, const void *base, int esz, int rank, const uint64_t *dims,
                       const uint64_t *strides, const uint32_t *box) {
   static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
     void *p = nullptr;
@@ -59,7 +59,9 @@ bool encode_sw128_map(CUtensorMap *m, const void *base, int esz, int rank, const
   }
   return fn(m, esz == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
             static_cast<cuuint32_t>(rank), const_cast<void *>(base), d, s, b, one,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE,
+            box[0] * static_cast<uint32_t>(esz) == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                      : CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
