@@ -18,6 +18,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 #include <mutex>
 
@@ -37,24 +38,40 @@ constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr size_t kSmemMost = 227 * 1024;
 constexpr uint64_t kDrainNs = 1000000000ull;
 
-// act() in fp32.  The exponential and the reciprocal are the hardware's
-// (relative error about 2^-21), far below the bf16 rounding of y.
-template <int N>
-__device__ __forceinline__ void activate(float (&v)[N], int act) {
-  if (act == CC3D_ACT_SILU) {
-#pragma unroll
-    for (int e = 0; e < N; ++e) v[e] = __fdividef(v[e], 1.f + __expf(-v[e]));
-  } else if (act == CC3D_ACT_GELU_TANH) {
-    // a (1 + tanh u) / 2 = a / (1 + exp(-2 u)), u = sqrt(2 / pi) (a + 0.044715 a^3)
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const float u2 = 1.5957691216057308f * fmaf(0.044715f * v[e] * v[e], v[e], v[e]);
-      v[e] = __fdividef(v[e], 1.f + __expf(-u2));
-    }
-  } else if (act == CC3D_ACT_GELU) {
-#pragma unroll
-    for (int e = 0; e < N; ++e) v[e] = 0.5f * v[e] * erfcf(v[e] * -0.70710678118654752f);
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// act() of a pair in fp32: a / (1 + 2^z) with z = -a log2(e) for SiLU, and for
+// the tanh form of GELU, a (1 + tanh u) / 2 = a / (1 + exp(-2 u)), z = -2 u
+// log2(e), u = sqrt(2 / pi) (a + 0.044715 a^3).  The exponential and the
+// reciprocal are the hardware's (relative error about 2^-21), far below the
+// bf16 rounding of y.
+__device__ __forceinline__ uint64_t activate(uint64_t a, int act) {
+  if (act == CC3D_ACT_NONE) return a;
+  if (act == CC3D_ACT_GELU) {
+    const float2 v = unpair(a);
+    return pair_of(0.5f * v.x * erfcf(v.x * -0.70710678118654752f),
+                   0.5f * v.y * erfcf(v.y * -0.70710678118654752f));
   }
+  uint64_t z;
+  if (act == CC3D_ACT_SILU) {
+    z = pair_mul(a, pair_of(-1.4426950408889634f, -1.4426950408889634f));
+  } else {
+    constexpr float k0 = -2.0f * 0.79788456080286536f * 1.4426950408889634f;
+    constexpr float k1 = 0.044715f * k0;
+    z = pair_mul(a, pair_fma(pair_mul(a, a), pair_of(k1, k1), pair_of(k0, k0)));
+  }
+  const float2 e = unpair(z);
+  const float2 d = unpair(pair_add(pair_of(ex2_approx(e.x), ex2_approx(e.y)), pair_of(1.f, 1.f)));
+  return pair_mul(a, pair_of(rcp_approx(d.x), rcp_approx(d.y)));
 }
 
 // Columns of y that an epilogue warp finishes at a time: rows of 64 bytes in
@@ -273,21 +290,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_load_2d(smem_u32(out) + buf * kOutBuf, &map_r, &res[buf],
                   nt * p.nt + half * cols + u * kOutCols, row0_of(mt));
     };
+    // bias and weight scale of columns lane, lane + 32, ..., the row's scale
+    float next_bias[4], next_scale[4], next_xs = 1.f;
+    auto fetch_params = [&](int t) {
+      int mt, nt;
+      walk.at(t, mt, nt);
+      const int c0 = nt * p.nt + half * cols + lane, row = row0_of(mt) + lane;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = c0 + 32 * i;
+        const bool used = i * 32 < cols && c < p.n;
+        next_bias[i] = p.bias && used ? p.bias[c] : 0.f;
+        if constexpr (FP8) next_scale[i] = used ? p.w_scales[c] : 0.f;
+      }
+      if constexpr (FP8)
+        next_xs = row < p.m ? (p.x_scales ? p.x_scales[row] : p.x_scale) : 1.f;
+    };
+    if (cid < n_tiles) fetch_params(cid);
     if (p.residual && lane == 0 && cid < n_tiles) fetch_residual(cid, 0, 0);
     for (int t = cid; t < n_tiles && ok; t += ncl, ++it) {
       int mt, nt;
       walk.at(t, mt, nt);
-      const int row = row0_of(mt) + lane;
       const int n0 = nt * p.nt + half * cols;
-      // the columns' parameters, while the MMAs run
+      // the columns' parameters where every lane reads them, and the next
+      // tile's on their way
       __syncwarp();
-      for (int i = lane; i < cols; i += 32) {
-        const int c = n0 + i;
-        s_bias[i] = p.bias && c < p.n ? p.bias[c] : 0.f;
-        if constexpr (FP8) s_scale[i] = c < p.n ? p.w_scales[c] : 0.f;
-      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i * 32 < cols) {
+          s_bias[i * 32 + lane] = next_bias[i];
+          if constexpr (FP8) s_scale[i * 32 + lane] = next_scale[i];
+        }
       __syncwarp();
-      const float xs = FP8 && row < p.m ? (p.x_scales ? p.x_scales[row] : p.x_scale) : 1.f;
+      const float xs = next_xs;
+      if (t + ncl < n_tiles) fetch_params(t + ncl);
       const int buf = it & 1;
       const uint32_t up = static_cast<uint32_t>((it >> 1) & 1);
       ok = __all_sync(0xffffffffu,
@@ -296,6 +332,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                              static_cast<uint32_t>(buf * p.nt + half * cols);
+      uint32_t raw[32];
+      tmem_ld32_nowait(taddr, raw);
       for (int u = 0; u < cols / kOutCols; ++u, ob ^= 1) {
         if (p.residual) {
           // the next buffer's worth (of this tile or the next one) on its way
@@ -306,13 +344,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = __all_sync(0xffffffffu, mbar_wait_bounded(&res[ob], (res_par >> ob) & 1u,
                                                          p.wait_limit_ns, p.status, 27));
           res_par ^= 1u << ob;
-          if (!ok) break;
+          if (!ok) {
+            tmem_wait_ld();  // (on their way to registers)
+            break;
+          }
         } else {
           if (lane == 0) bulk_groups_wait_read<1>();
           __syncwarp();
         }
-        uint32_t raw[32];
-        tmem_ld32_nowait(taddr + u * kOutCols, raw);
         tmem_wait_ld();
         tmem_regs_after_wait<32>(raw);
         if ((u + 1) * kOutCols == cols) {
@@ -325,38 +364,39 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float *bias = s_bias + u * kOutCols, *scale = s_scale + u * kOutCols;
+        float acc[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) acc[e] = __uint_as_float(raw[e]);
+        if ((u + 1) * kOutCols < cols) tmem_ld32_nowait(taddr + (u + 1) * kOutCols, raw);
+        const uint64_t xs2 = pair_of(xs, xs);
 #pragma unroll
         for (int g = 0; g < kOutCols; g += 8) {
-          float v[8];
-          const float4 b0 = *reinterpret_cast<const float4 *>(bias + g);
-          const float4 b1 = *reinterpret_cast<const float4 *>(bias + g + 4);
-          const float bs[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
-          if constexpr (FP8) {
-            const float4 s0 = *reinterpret_cast<const float4 *>(scale + g);
-            const float4 s1 = *reinterpret_cast<const float4 *>(scale + g + 4);
-            const float ws[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              v[e] = fmaf(__uint_as_float(raw[g + e]), xs * ws[e], bs[e]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(raw[g + e]) + bs[e];
-          }
-          activate(v, p.act);
           uint4 *at = piece(ob, g / 8);
+          uint32_t rw[4] = {0u, 0u, 0u, 0u}, o[4];
           if (p.residual) {
             const uint4 r4 = *at;
-            const uint32_t rw[4] = {r4.x, r4.y, r4.z, r4.w};
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              v[e] += __uint_as_float(e & 1 ? rw[e / 2] & 0xffff0000u : rw[e / 2] << 16);
+            rw[0] = r4.x;
+            rw[1] = r4.y;
+            rw[2] = r4.z;
+            rw[3] = r4.w;
           }
-          uint4 o;
-          o.x = pack_bf16x2(v[0], v[1]);
-          o.y = pack_bf16x2(v[2], v[3]);
-          o.z = pack_bf16x2(v[4], v[5]);
-          o.w = pack_bf16x2(v[6], v[7]);
-          *at = o;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int i = g + 2 * e;
+            const uint64_t b2 = *reinterpret_cast<const uint64_t *>(bias + i);
+            uint64_t v = pair_of(acc[i], acc[i + 1]);
+            if constexpr (FP8)
+              v = pair_fma(v, pair_mul(xs2, *reinterpret_cast<const uint64_t *>(scale + i)), b2);
+            else
+              v = pair_add(v, b2);
+            v = activate(v, p.act);
+            if (p.residual)
+              v = pair_add(v, pair_of(__uint_as_float(rw[e] << 16),
+                                      __uint_as_float(rw[e] & 0xffff0000u)));
+            const float2 f = unpair(v);
+            o[e] = pack_bf16x2(f.x, f.y);
+          }
+          *at = make_uint4(o[0], o[1], o[2], o[3]);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -558,7 +598,11 @@ __global__ void __launch_bounds__(kSplitThreads)
       }
       v[0] += b0;
       v[1] += b1;
-      activate(v, p.act);
+      {
+        const float2 f = unpair(activate(pair_of(v[0], v[1]), p.act));
+        v[0] = f.x;
+        v[1] = f.y;
+      }
       if (p.residual) {
         const uint32_t rw = *reinterpret_cast<const uint32_t *>(p.residual + row * p.ldr + c);
         v[0] += __uint_as_float(rw << 16);
@@ -572,139 +616,166 @@ __global__ void __launch_bounds__(kSplitThreads)
 
 // ---- choice of kernel and tile -----------------------------------------------------
 
+using LinearKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap,
+                              const CUtensorMap, const LinearArgs);
+using SplitKernel = void (*)(const CUtensorMap, const CUtensorMap, const LinearArgs);
+
+const LinearKernel kLinear[2][2] = {{linear_kernel<false, false>, linear_kernel<false, true>},
+                                    {linear_kernel<true, false>, linear_kernel<true, true>}};
+const SplitKernel kSplit[2] = {linear_split_kernel<false>, linear_split_kernel<true>};
+
 struct Choice {
   bool split_kernel;
   int pair, nt, stages, split;
 };
 
-// Relative times in cycles of one SM: a chunk costs its MMAs (a 128 x NT x
-// 64 chunk NT * 2 cycles) or its bytes, a tile an epilogue that the next
-// tile's MMAs hide.
-Choice choose(const LinearArgs &a, bool fp8, int sm_count) {
-  const int nk = (a.k + (fp8 ? 127 : 63)) / (fp8 ? 128 : 64);
-  Choice best = {};
-  double best_t = 1e300;
-  // many rows
-  const int shapes[4][2] = {{1, 256}, {1, 128}, {0, 128}, {0, 64}};
-  for (const auto &sh : shapes) {
-    const int pair = sh[0], nt = sh[1], rows = pair ? 256 : 128;
-    const double tiles = static_cast<double>((a.m + rows - 1) / rows) * ((a.n + nt - 1) / nt);
-    const int slots = pair ? sm_count / 2 : sm_count;
-    const double rounds = static_cast<double>(static_cast<long long>((tiles + slots - 1) / slots));
-    const double bytes = kAStage + (pair ? nt / 2 : nt) * static_cast<double>(kRowBytes);
-    const double mma = nt * 2.0, load = bytes / 64.0;
-    const double epi = 64.0 + nt * (a.act ? 14.0 : 8.0);
-    const double per = nk * (mma > load ? mma : load);
-    const double t = 3000.0 + epi + rounds * (per > epi ? per : epi);
-    if (t < best_t) {
-      best_t = t;
-      best = Choice{false, pair, nt, 0, 1};
-    }
-  }
-  // few rows: clusters split K until every SM streams weights
-  if (a.m <= 512) {
-    int nt = 16;
-    while (nt < a.m && nt < 128) nt += 16;
-    const int tiles = ((a.n + 127) / 128) * ((a.m + nt - 1) / nt);
-    for (int split = 1; split <= 8 && split <= nk; ++split) {
-      const double ctas = static_cast<double>(tiles) * split;
-      const double rounds = static_cast<double>(static_cast<long long>((ctas + 2 * sm_count - 1) / (2 * sm_count)));
-      const double share = ctas < sm_count ? 1.0 : 2.0;  // CTAs of one SM
-      const double bytes = kAStage + nt * static_cast<double>(kRowBytes);
-      const double chunks = (nk + split - 1) / split;
-      const double t = 3500.0 + (split > 1 ? 800.0 : 0.0) +
-                       rounds * (1000.0 + share * chunks * (bytes / 32.0 > nt * 2.0 ? bytes / 32.0
-                                                                                   : nt * 2.0) +
-                                 share * nt * 20.0 / split);
-      if (t < best_t) {
-        best_t = t;
-        best = Choice{true, 0, nt, 0, split};
-      }
-    }
-  }
-  if (best.split_kernel) {
-    // two CTAs per SM
-    best.stages = 8;
-    while (best.stages > 2 && split_total(best.nt, best.stages) + 1024 > kSmemMost / 2 - 1024)
-      --best.stages;
-  } else {
-    best.stages = 8;
-    while (ring_layout(best.pair ? best.nt / 2 : best.nt, best.stages, best.nt).total + 1024 >
-           kSmemMost)
-      --best.stages;
-  }
-  return best;
+int many_stages(int pair, int nt) {
+  int st = 8;
+  while (ring_layout(pair ? nt / 2 : nt, st, nt).total + 1024 > kSmemMost) --st;
+  return st;
+}
+int split_stages(int nt) {
+  // two CTAs per SM
+  int st = 8;
+  while (st > 2 && split_total(nt, st) + 1024 > kSmemMost / 2 - 1024) --st;
+  return st;
 }
 
-using LinearKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap,
-                              const CUtensorMap, const LinearArgs);
-using SplitKernel = void (*)(const CUtensorMap, const CUtensorMap, const LinearArgs);
-
-// Pairs of CTAs that can be resident at once, per device (grid of the
-// persistent pair kernel).
-int max_pairs(LinearKernel k, size_t smem, int sm_count) {
-  static std::mutex mu;
-  static int known[64][2] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return sm_count / 2;
-  const int which = k == linear_kernel<true, true>;
-  std::lock_guard<std::mutex> lk(mu);
-  if (!known[dev][which]) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, reinterpret_cast<const void *>(k), &cfg) !=
-            cudaSuccess ||
-        n < 1) {
-      (void)cudaGetLastError();
-      n = sm_count / 2;
-    }
-    known[dev][which] = n;
+cudaLaunchConfig_t launch_config(unsigned grid, unsigned block, size_t smem, unsigned cluster,
+                                 cudaLaunchAttribute *attr, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  unsigned n = 0;
+  attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  if (cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = cluster;
+    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+    ++n;
   }
-  return known[dev][which];
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  return cfg;
 }
 
-cudaError_t prepare_kernels() {
-  // per device: the kernels' shared-memory limit
-  static std::mutex mu;
-  static bool done[64] = {false};
+// Per device, on first use: the kernels' shared-memory limit, how many CTA
+// pairs of the persistent kernel and how many clusters of the split kernel
+// (by N tile / 16 and split) are resident at once.
+struct Prepared {
+  bool done;
+  int pairs[2];
+  int clusters[2][9][9];
+};
+std::mutex g_prepare_mu;
+Prepared g_prepared[64];
+
+int resident(const void *k, unsigned block, size_t smem, unsigned cluster, int otherwise) {
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = launch_config(cluster, block, smem, cluster, attr, nullptr);
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess || n < 1) {
+    (void)cudaGetLastError();
+    return otherwise;
+  }
+  return n;
+}
+
+cudaError_t prepare_kernels(int sm_count, const Prepared **out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  std::lock_guard<std::mutex> lk(mu);
-  if (done[dev]) return cudaSuccess;
-  const void *ks[6] = {reinterpret_cast<const void *>(&linear_kernel<false, false>),
-                       reinterpret_cast<const void *>(&linear_kernel<false, true>),
-                       reinterpret_cast<const void *>(&linear_kernel<true, false>),
-                       reinterpret_cast<const void *>(&linear_kernel<true, true>),
-                       reinterpret_cast<const void *>(&linear_split_kernel<false>),
-                       reinterpret_cast<const void *>(&linear_split_kernel<true>)};
-  for (const void *k : ks) {
-    e = cudaFuncSetAttribute(k,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kSmemMost));
-    if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lk(g_prepare_mu);
+  Prepared &p = g_prepared[dev];
+  if (!p.done) {
+    for (int f = 0; f < 2; ++f) {
+      const void *ks[3] = {reinterpret_cast<const void *>(kLinear[f][0]),
+                           reinterpret_cast<const void *>(kLinear[f][1]),
+                           reinterpret_cast<const void *>(kSplit[f])};
+      for (const void *k : ks) {
+        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(kSmemMost));
+        if (e != cudaSuccess) return e;
+      }
+      p.pairs[f] = resident(ks[1], kThreads, kSmemMost, 2, sm_count / 2);
+      for (int n = 1; n <= 8; ++n)
+        for (int s = 1; s <= 8; ++s)
+          p.clusters[f][n][s] =
+              s == 1 ? 2 * sm_count
+                     : resident(ks[2], kSplitThreads,
+                                split_total(16 * n, split_stages(16 * n)) + 1024,
+                                static_cast<unsigned>(s), 0);
+    }
+    p.done = true;
   }
-  done[dev] = true;
+  *out = &p;
   return cudaSuccess;
+}
+
+// Estimated cycles, from measurements of both kernels at K = 384 to 8192 and 1
+// to 16384 rows.  Many rows: rounds of tiles, each the longest of its products
+// (four a chunk, N / 2 + 44 cycles), its operands (68 bytes a cycle and SM from
+// L2) and its epilogue.  Few rows: the operands' bytes at 45 a cycle and SM and
+// at 3500 from HBM, and the joining of the parts.
+Choice choose(const LinearArgs &a, bool fp8, int sm_count, const Prepared &pre) {
+  const int nk = (a.k + (fp8 ? 127 : 63)) / (fp8 ? 128 : 64);
+  Choice best = {};
+  double best_t = 1e300;
+  const int shapes[4][2] = {{1, 256}, {1, 128}, {0, 128}, {0, 64}};
+  for (const auto &sh : shapes) {
+    const int pair = sh[0], nt = sh[1], rows = pair ? 256 : 128;
+    const double tiles = static_cast<double>((a.m + rows - 1) / rows) * ((a.n + nt - 1) / nt);
+    const int slots = pair ? pre.pairs[fp8] : sm_count;
+    const double rounds = std::ceil(tiles / slots);
+    const double bytes = kAStage + (pair ? nt / 2 : nt) * static_cast<double>(kRowBytes);
+    const double epi = 600.0 + nt * (a.act == CC3D_ACT_NONE ? 14.0 : 30.0);
+    double per = nk * 4.0 * (nt / 2.0 + 44.0);
+    per = std::fmax(per, nk * bytes / 68.0);
+    per = std::fmax(per, epi);
+    const double t = 5500.0 + 1000.0 * pair + epi + rounds * (per + 500.0);
+    if (t < best_t) {
+      best_t = t;
+      best = Choice{false, pair, nt, many_stages(pair, nt), 1};
+    }
+  }
+  if (a.m <= 512) {
+    int nt = 16;
+    while (nt < a.m && nt < 128) nt += 16;
+    for (; nt >= 64 || nt >= a.m; nt -= 64) {  // (the tokens' own tile, and a half of 128)
+      const double tiles = static_cast<double>((a.n + 127) / 128) * ((a.m + nt - 1) / nt);
+      const double hbm = (static_cast<double>(a.n) + a.m) * nk * kRowBytes / 3500.0;
+      const double bytes = kAStage + nt * static_cast<double>(kRowBytes);
+      for (int split = 1; split <= 8 && split <= nk; ++split) {
+        const int fit = pre.clusters[fp8][nt / 16][split];
+        if (fit < 1) continue;
+        const double waves = std::ceil(tiles / fit);
+        const double share = tiles * split > sm_count ? 1.8 : 1.0;  // two CTAs of an SM
+        const double stream = waves * std::ceil(static_cast<double>(nk) / split) * bytes * share / 45.0;
+        const double t = 5400.0 + (split > 1 ? 800.0 : 0.0) + 50.0 * split + 30.0 * nt +
+                         std::hypot(hbm, stream) + 900.0 * (waves - 1.0);
+        if (t < best_t) {
+          best_t = t;
+          best = Choice{true, 0, nt, split_stages(nt), split};
+        }
+      }
+      if (nt <= 64) break;
+    }
+  }
+  return best;
 }
 
 }  // namespace
 
 cudaError_t launch_linear(LinearArgs a, const void *x, long long ldx, const void *w,
                           long long ldw, bool fp8, int sm_count, cudaStream_t stream) {
-  cudaError_t e = prepare_kernels();
+  const Prepared *pre = nullptr;
+  cudaError_t e = prepare_kernels(sm_count, &pre);
   if (e != cudaSuccess) return e;
-  const Choice c = choose(a, fp8, sm_count);
+  const Choice c = choose(a, fp8, sm_count, *pre);
   a.nt = c.nt;
   a.stages = c.stages;
   a.split = c.split;
@@ -720,64 +791,38 @@ cudaError_t launch_linear(LinearArgs a, const void *x, long long ldx, const void
   const uint32_t bx[2] = {chunk, x_rows}, bw[2] = {chunk, w_rows};
   if (!encode_rows_map(&mx, x, esz, 2, dx, sx, bx) || !encode_rows_map(&mw, w, esz, 2, dw, sw, bw))
     return cudaErrorInvalidValue;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[2];
-  unsigned na = 0;
-  attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[na].val.programmaticStreamSerializationAllowed = 1;
-  ++na;
-  LinearKernel k = nullptr;
-  SplitKernel ks = nullptr;
-  unsigned cluster = 1;
-  CUtensorMap my, mr;
-  if (!c.split_kernel) {
-    const uint64_t dy[2] = {static_cast<uint64_t>(a.n), static_cast<uint64_t>(a.m)};
-    const uint64_t sy[1] = {static_cast<uint64_t>(a.ldy) * 2};
-    const uint64_t sr[1] = {static_cast<uint64_t>(a.ldr) * 2};
-    const uint32_t by[2] = {kOutCols, 32};
-    if (!encode_rows_map(&my, a.y, 2, 2, dy, sy, by)) return cudaErrorInvalidValue;
-    mr = my;
-    if (a.residual && !encode_rows_map(&mr, a.residual, 2, 2, dy, sr, by))
-      return cudaErrorInvalidValue;
-  }
-  if (c.split_kernel) {
-    ks = fp8 ? linear_split_kernel<true> : linear_split_kernel<false>;
-    const unsigned tiles = static_cast<unsigned>(((a.n + 127) / 128) * ((a.m + c.nt - 1) / c.nt));
-    cfg.gridDim = dim3(tiles * c.split);
-    cfg.blockDim = dim3(kSplitThreads);
-    cfg.dynamicSmemBytes = split_total(c.nt, c.stages) + 1024;
-    cluster = c.split;
-  } else {
-    const size_t smem = ring_layout(c.pair ? c.nt / 2 : c.nt, c.stages, c.nt).total + 1024;
-    const int rows = c.pair ? 256 : 128;
-    const long long tiles =
-        static_cast<long long>((a.m + rows - 1) / rows) * ((a.n + c.nt - 1) / c.nt);
-    if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
-    if (c.pair) {
-      k = fp8 ? linear_kernel<true, true> : linear_kernel<false, true>;
-      const long long pairs = max_pairs(k, kSmemMost, sm_count);
-      cfg.gridDim = dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)));
-      cluster = 2;
-    } else {
-      k = fp8 ? linear_kernel<true, false> : linear_kernel<false, false>;
-      cfg.gridDim = dim3(static_cast<unsigned>(tiles < sm_count ? tiles : sm_count));
-    }
-    cfg.blockDim = dim3(kThreads);
-    // (more than half an SM: one CTA per SM, which the tensor memory wants)
-    cfg.dynamicSmemBytes = smem;
-  }
-  if (cluster > 1) {
-    attr[na].id = cudaLaunchAttributeClusterDimension;
-    attr[na].val.clusterDim.x = cluster;
-    attr[na].val.clusterDim.y = attr[na].val.clusterDim.z = 1;
-    ++na;
-  }
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = na;
   const LinearArgs args = a;
-  e = ks ? cudaLaunchKernelEx(&cfg, ks, mx, mw, args)
-         : cudaLaunchKernelEx(&cfg, k, mx, mw, my, mr, args);
+  cudaLaunchAttribute attr[2];
+  if (c.split_kernel) {
+    const unsigned tiles = static_cast<unsigned>(((a.n + 127) / 128) * ((a.m + c.nt - 1) / c.nt));
+    const cudaLaunchConfig_t cfg =
+        launch_config(tiles * c.split, kSplitThreads, split_total(c.nt, c.stages) + 1024,
+                      static_cast<unsigned>(c.split), attr, stream);
+    e = cudaLaunchKernelEx(&cfg, kSplit[fp8], mx, mw, args);
+    count_launch();
+    return e;
+  }
+  CUtensorMap my, mr;
+  const uint64_t dy[2] = {static_cast<uint64_t>(a.n), static_cast<uint64_t>(a.m)};
+  const uint64_t sy[1] = {static_cast<uint64_t>(a.ldy) * 2};
+  const uint64_t sr[1] = {static_cast<uint64_t>(a.ldr) * 2};
+  const uint32_t by[2] = {kOutCols, 32};
+  if (!encode_rows_map(&my, a.y, 2, 2, dy, sy, by)) return cudaErrorInvalidValue;
+  mr = my;
+  if (a.residual && !encode_rows_map(&mr, a.residual, 2, 2, dy, sr, by))
+    return cudaErrorInvalidValue;
+  const int rows = c.pair ? 256 : 128;
+  const long long tiles =
+      static_cast<long long>((a.m + rows - 1) / rows) * ((a.n + c.nt - 1) / c.nt);
+  if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
+  const long long slots = c.pair ? pre->pairs[fp8] : sm_count;
+  const unsigned cluster = c.pair ? 2u : 1u;
+  // (more than half an SM's shared memory: one CTA per SM, which the tensor
+  // memory wants)
+  const cudaLaunchConfig_t cfg = launch_config(
+      static_cast<unsigned>(tiles < slots ? tiles : slots) * cluster, kThreads,
+      ring_layout(c.pair ? c.nt / 2 : c.nt, c.stages, c.nt).total + 1024, cluster, attr, stream);
+  e = cudaLaunchKernelEx(&cfg, kLinear[fp8][c.pair], mx, mw, my, mr, args);
   count_launch();
   return e;
 }
