@@ -154,12 +154,15 @@ __device__ __forceinline__ void lengths(const CacheShape &c, int seq, int &chunk
 }
 
 // Shapes of a kernel: NQ row tiles of 128, key tiles of KT tokens, CH chunks
-// of 64 channels.  Keys and values travel in groups of GC chunks (one
-// barrier, one N = 64 GC product step of P V), NG groups a tile.
+// of 64 channels.  Keys and values travel in groups of GC chunks, NG a tile,
+// one barrier each: whole tiles where several fit beside Q, single chunks for
+// wide heads (a slot is then free, and its next load on its way, as soon as
+// four products have read it).  P V runs in steps of PC chunks (N = 64 PC).
 template <int NQ, int KT, int CH>
 struct Shape {
-  static constexpr int GC = CH <= 2 ? CH : CH / 2;
+  static constexpr int GC = CH <= 2 ? CH : 1;
   static constexpr int NG = CH / GC;
+  static constexpr int PC = CH <= 2 ? CH : 2;
   static constexpr uint32_t kChunk = KT * 128u;
   static constexpr uint32_t kGroup = GC * kChunk;
   static constexpr uint32_t kQ = NQ * CH * kQChunk;
@@ -170,7 +173,8 @@ struct Shape {
   }
   static constexpr int stages() {
     int st = 24;
-    while (kQ + st * kGroup + rest(st) > kSmemMost) --st;
+    // (whole steps of P V side by side)
+    while (kQ + st * kGroup + rest(st) > kSmemMost || st % (PC / GC) != 0) --st;
     return st;
   }
   static constexpr int kStages = stages();
@@ -322,8 +326,9 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
   constexpr uint32_t o_cols = CH * 64u;
   const uint32_t o_col = tmem + 2 * NQ * KT;
   griddep_launch_dependents();
-  // (the lengths too may come from an earlier kernel of the stream)
-  griddep_wait();
+  // Earlier kernels of the stream may still write what is read here (the
+  // lengths at once, the rest where it is loaded) or read what is written.
+  if (cs.k_frames || cs.q_frames) griddep_wait();
 
   // What this CTA (or cluster) works on: query tokens tok0 .. tok_end - 1 of
   // one sequence and kv head.
@@ -366,6 +371,7 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
     // ------------------------------ loads ---------------------------------------
     if constexpr (NQ == 2) regs_fewer<kRegsFew>();
     if (nj > 0 && elect_one()) {
+      griddep_wait();
       const int rows = p.tok_tile * p.group;
       mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(NQ * CH * rows) * 128u);
       for (int q = 0; q < NQ; ++q)
@@ -408,7 +414,7 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
     if constexpr (NQ == 2) regs_fewer<kRegsFew>();
     if (nj > 0 && elect_one()) {
       constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, KT);
-      constexpr uint32_t idesc_o = idesc_bf16_f32_bt(kRows, 64 * GC);
+      constexpr uint32_t idesc_o = idesc_bf16_f32_bt(kRows, 64 * S::PC);
       const uint64_t qd = smem_desc_sw128(smem_base, 1024u);
       const uint64_t kd = smem_desc_sw128(ring, 1024u);
       const uint64_t vd = smem_desc_sw128_mn(ring, S::kChunk, 1024u);
@@ -429,57 +435,43 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
         if (ok && !mbar_wait_bounded(bar, parity, p.wait_limit_ns, p.status, site)) ok = false;
         return ok;
       };
-      auto await_tile = [&](Pos x, int site) {
+      // S[q][slot] = Q[q] K^T, a group at a time as it arrives
+      auto scores = [&](int q, int slot, Pos x) {
+        const uint32_t col = s_col(q, slot);
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          await(&full[x.slot], x.phase, site);
-          x = next(x);
-        }
-      };
-      // (after the MMAs that read them)
-      auto release_tile = [&](Pos x) {
+          if (!await(&full[x.slot], x.phase, 31)) return;
+          const uint64_t b = kd + ((x.slot * S::kGroup) >> 4);
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
+          for (int i = 0; i < 4 * GC; ++i) {
+            const int c = g * GC + i / 4, k = i % 4;
+            umma_bf16(col, qd + ((static_cast<uint32_t>(q * CH + c) * kQChunk) >> 4) + 2 * k,
+                      b + (((i / 4) * S::kChunk) >> 4) + 2 * k, idesc_s, g > 0 || i > 0);
+          }
           umma_commit(&empty[x.slot]);
           x = next(x);
         }
-      };
-      constexpr int kSteps = KT / 16;
-      // the i-th product of S[q][slot] = Q[q] K^T, of O[q] (+)= P[q][slot] V
-      struct Desc {
-        uint64_t d[NG];
-      };
-      auto desc_of = [&](uint64_t base_desc, Pos x) {
-        Desc r;
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-          r.d[g] = base_desc + ((x.slot * S::kGroup) >> 4);
-          x = next(x);
-        }
-        return r;
-      };
-      auto score_step = [&](int q, uint32_t col, const Desc &b, int i) {
-        const int c = i / 4, k = i % 4;
-        umma_bf16(col, qd + ((static_cast<uint32_t>(q * CH + c) * kQChunk) >> 4) + 2 * k,
-                  b.d[c / GC] + (((c % GC) * S::kChunk) >> 4) + 2 * k, idesc_s, i > 0);
-      };
-      auto value_step = [&](int q, uint32_t col, const Desc &b, int i, bool first) {
-        const int g = i / kSteps, k = i % kSteps;
-        umma_bf16_ta(o_col + q * o_cols + g * GC * 64, col + 8 * k, b.d[g] + 128 * k, idesc_o,
-                     !first || k > 0);
-      };
-      auto scores = [&](int q, int slot, Pos k) {
-        const Desc b = desc_of(kd, k);
-        const uint32_t col = s_col(q, slot);
-#pragma unroll
-        for (int i = 0; i < 4 * CH; ++i) score_step(q, col, b, i);
         umma_commit(&s_full[2 * q + slot]);
       };
-      auto values = [&](int q, int slot, Pos v, bool first) {
-        const Desc b = desc_of(vd, v);
+      // O[q] (+)= P[q][slot] V
+      auto values = [&](int q, int slot, Pos x, bool first) {
         const uint32_t col = s_col(q, slot);
 #pragma unroll
-        for (int i = 0; i < NG * kSteps; ++i) value_step(q, col, b, i, first);
+        for (int c = 0; c < CH; c += S::PC) {
+          const int at = x.slot;
+#pragma unroll
+          for (int u = 0; u < S::PC / GC; ++u) {
+            if (!await(&full[x.slot], x.phase, 32)) return;
+            x = next(x);
+          }
+          const uint64_t b = vd + ((at * S::kGroup) >> 4);
+#pragma unroll
+          for (int k = 0; k < KT / 16; ++k)
+            umma_bf16_ta(o_col + q * o_cols + c * 64, col + 8 * k, b + 128 * k, idesc_o,
+                         !first || k > 0);
+#pragma unroll
+          for (int u = 0; u < S::PC / GC; ++u) umma_commit(&empty[at + u]);
+        }
         umma_commit(&pv_done[2 * q + slot]);
       };
       await(q_full, 0, 34);
@@ -490,24 +482,17 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
         // each row tile's products from a warp of their own
         const int q = warp - 1;
         for (int j = 0; j < 2 && j < nj && ok; ++j) {
-          await_tile(k, 31);
-          if (!ok) break;
           scores(q, j, k);
-          release_tile(k);
           advance(k, 1 + j);  // (past V 0)
         }
 #pragma unroll 1
         for (int j = 0; j < nj && ok; ++j) {
-          await_tile(v, 32);
-          if (j + 2 < nj) await_tile(k, 31);
           if (!await(&p_ready[2 * q + (j & 1)], (j >> 1) & 1, 33)) break;
           tc_fence_after();
           values(q, j & 1, v, j == 0);
-          release_tile(v);
           advance(v, j + 2 < nj ? 2 : 1);
-          if (j + 2 < nj) {
+          if (j + 2 < nj && ok) {
             scores(q, j & 1, k);
-            release_tile(k);
             advance(k, 2);
           }
         }
@@ -515,22 +500,17 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
         // the two kinds of products from a warp each
 #pragma unroll 1
         for (int j = 0; j < nj && ok; ++j) {
-          await_tile(k, 31);
           if (j >= 2 && !await(&pv_done[j & 1], ((j >> 1) - 1) & 1, 39)) break;
-          if (!ok) break;
           tc_fence_after();
           scores(0, j & 1, k);
-          release_tile(k);
           advance(k, j == 0 ? 1 : 2);
         }
       } else {
 #pragma unroll 1
         for (int j = 0; j < nj && ok; ++j) {
-          await_tile(v, 32);
           if (!await(&p_ready[j & 1], (j >> 1) & 1, 33)) break;
           tc_fence_after();
           values(0, j & 1, v, j == 0);
-          release_tile(v);
           advance(v, j + 2 < nj ? 2 : 1);
         }
       }
@@ -686,35 +666,51 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
       tc_fence_after();
     }
     if (split == 1 && ok) {
+      // 64 channels of the warp's 32 rows at a time through shared memory (Q's,
+      // which every product has read), so that eight lanes store a row's 128
+      // bytes.
       __nv_bfloat16 *out = p.o + static_cast<long long>(seq) * p.o_seq +
                            static_cast<long long>(tok) * p.o_tok +
                            static_cast<long long>(head) * p.o_head;
       const float inv = (l > 0.f || l != l) ? 1.f / l : 0.f;
       const uint32_t o = o_col + wg * o_cols + lanes;
-      for (int i = 0; i < cs.d; i += 32) {
-        __syncwarp();
-        uint32_t v[32];
-        if (nj > 0) {
-          tmem_ld32_nowait(o + i, v);
-          tmem_wait_ld();
-          tmem_regs_after_wait<32>(v);
-        }
-        // (a row that saw nothing gives zeros, whatever the accumulator holds)
+      uint8_t *stage = smem + static_cast<uint32_t>(wg * CH) * kQChunk + quarter * 4096u;
+      griddep_wait();
+#pragma unroll 1
+      for (int i = 0; i < cs.d; i += 64) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-          v[e] = inv == 0.f ? 0u : __float_as_uint(__uint_as_float(v[e]) * inv);
-        if (live) {
+        for (int h = 0; h < 64; h += 32) {
+          uint32_t v[32];
+          if (nj > 0) {
+            tmem_ld32_nowait(o + i + h, v);
+            tmem_wait_ld();
+            tmem_regs_after_wait<32>(v);
+          }
+          // (a row that saw nothing gives zeros, whatever the accumulator holds)
 #pragma unroll
-          for (int h = 0; h < 32; h += 8) {
-            if (i + h >= cs.d) break;
+          for (int e = 0; e < 32; ++e)
+            v[e] = inv == 0.f ? 0u : __float_as_uint(__uint_as_float(v[e]) * inv);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
             uint4 w;
-            w.x = pack_bf16x2(__uint_as_float(v[h]), __uint_as_float(v[h + 1]));
-            w.y = pack_bf16x2(__uint_as_float(v[h + 2]), __uint_as_float(v[h + 3]));
-            w.z = pack_bf16x2(__uint_as_float(v[h + 4]), __uint_as_float(v[h + 5]));
-            w.w = pack_bf16x2(__uint_as_float(v[h + 6]), __uint_as_float(v[h + 7]));
-            *reinterpret_cast<uint4 *>(out + i + h) = w;
+            w.x = pack_bf16x2(__uint_as_float(v[8 * e]), __uint_as_float(v[8 * e + 1]));
+            w.y = pack_bf16x2(__uint_as_float(v[8 * e + 2]), __uint_as_float(v[8 * e + 3]));
+            w.z = pack_bf16x2(__uint_as_float(v[8 * e + 4]), __uint_as_float(v[8 * e + 5]));
+            w.w = pack_bf16x2(__uint_as_float(v[8 * e + 6]), __uint_as_float(v[8 * e + 7]));
+            *reinterpret_cast<uint4 *>(stage + lane * 128 + (((h / 8 + e) ^ (lane & 7)) << 4)) = w;
           }
         }
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int from = 4 * u + lane / 8, piece = lane % 8;  // row of the warp, 16 bytes of it
+          const unsigned long long at = __shfl_sync(
+              0xffffffffu, live ? reinterpret_cast<unsigned long long>(out) : 0ull, from);
+          if (at != 0 && i + 8 * piece < cs.d)
+            *reinterpret_cast<uint4 *>(reinterpret_cast<__nv_bfloat16 *>(at) + i + 8 * piece) =
+                *reinterpret_cast<const uint4 *>(stage + from * 128 + ((piece ^ (from & 7)) << 4));
+        }
+        __syncwarp();
       }
     }
     if (split > 1) row_ml[wg * kRows + r] = make_float2(m, l);
@@ -728,6 +724,7 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
     // its shared memory (the keys are done with), and finishes the rows rank,
     // rank + split, ...
     const int pitch = cs.d + 4;  // floats: rows start in different banks
+    constexpr int kPieces = (CH + 1) / 2;
     float *part = reinterpret_cast<float *>(smem);
     const int tile_rows = p.tok_tile * p.group;  // used rows of a row tile
     if (warp >= kFirstRowWarp) {
@@ -745,24 +742,24 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
       float f = 0.f;
       if (me.x != -INFINITY && (all > 0.f || all != all))
         f = exp2_fast((me.x - top) * p.scale_log2) / all;
-      const uint32_t o =
-          o_col + wg * o_cols + (static_cast<uint32_t>((warp % 4) * 32) << 16);
+      const uint32_t o = o_col + wg * o_cols + (static_cast<uint32_t>((warp % 4) * 32) << 16);
       const bool have = ok && nj > 0;
       float *dst = part + (wg * kRows + r) * pitch;
-      for (int i = 0; i < cs.d; i += 16) {
+#pragma unroll 1
+      for (int i = 0; i < cs.d; i += 32) {
         __syncwarp();
-        uint32_t v[16];
+        uint32_t v[32];
         if (have) {
-          tmem_ld16_nowait(o + i, v);
+          tmem_ld32_nowait(o + i, v);
           tmem_wait_ld();
-          tmem_regs_after_wait<16>(v);
+          tmem_regs_after_wait<32>(v);
         }
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
+        for (int e = 0; e < 32; ++e)
           v[e] = (have && f != 0.f) ? __float_as_uint(__uint_as_float(v[e]) * f) : 0u;
         if (r < tile_rows) {
 #pragma unroll
-          for (int e = 0; e < 16; e += 4)
+          for (int e = 0; e < 32; e += 4)
             if (i + e < cs.d)
               *reinterpret_cast<uint4 *>(dst + i + e) =
                   make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
@@ -771,31 +768,44 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
     }
     __syncwarp();
     cluster_sync();
-    const int rows = max(0, tok_end - tok0) * p.group;  // rows of all row tiles
-    const int per = cs.d / 4;
-    const int count = (rows - rank + split - 1) / split;  // this rank's
-    for (int x = threadIdx.x; x < count * per; x += blockDim.x) {
-      const int row = rank + x / per * split, i = (x % per) * 4;
+    griddep_wait();
+    // a warp a row, a lane four channels at a time, every rank's on their way
+    // before the first is added
+    const int rows = max(0, tok_end - tok0) * p.group;  // of all row tiles
+    const int warps = static_cast<int>(blockDim.x) / 32;
+    for (int row = rank + split * warp; row < rows; row += split * warps) {
       const int q = row / tile_rows, r = row - q * tile_rows;
+      const int tk = row / p.group;
+      __nv_bfloat16 *out = p.o + static_cast<long long>(seq) * p.o_seq +
+                           static_cast<long long>(tok0 + tk) * p.o_tok +
+                           static_cast<long long>(kv_head * p.group + row - tk * p.group) * p.o_head;
       const uint32_t at =
-          smem_base + static_cast<uint32_t>((q * kRows + r) * pitch + i) * 4u;
-      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int k = 0; k < split; ++k) {
-        const uint32_t from = mapa_shared(at, k);
-        const float2 a = ld_cluster_f32x2(from), b = ld_cluster_f32x2(from + 8);
-        sum.x += a.x;
-        sum.y += a.y;
-        sum.z += b.x;
-        sum.w += b.y;
-      }
-      uint2 w;
-      w.x = pack_bf16x2(sum.x, sum.y);
-      w.y = pack_bf16x2(sum.z, sum.w);
-      *reinterpret_cast<uint2 *>(p.o + static_cast<long long>(seq) * p.o_seq +
-                                 static_cast<long long>(tok0 + row / p.group) * p.o_tok +
-                                 static_cast<long long>(kv_head * p.group + row % p.group) *
-                                     p.o_head +
-                                 i) = w;
+          smem_base + static_cast<uint32_t>((q * kRows + r) * pitch + 4 * lane) * 4u;
+      float4 v[kPieces][8];
+#pragma unroll
+      for (int c = 0; c < kPieces; ++c)
+        if (c * 128 + 4 * lane < cs.d) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (k < split) v[c][k] = ld_cluster_f32x4(mapa_shared(at + c * 512u, k));
+        }
+#pragma unroll
+      for (int c = 0; c < kPieces; ++c)
+        if (c * 128 + 4 * lane < cs.d) {
+          float4 sum = v[c][0];
+#pragma unroll
+          for (int k = 1; k < 8; ++k)
+            if (k < split) {
+              sum.x += v[c][k].x;
+              sum.y += v[c][k].y;
+              sum.z += v[c][k].z;
+              sum.w += v[c][k].w;
+            }
+          uint2 w;
+          w.x = pack_bf16x2(sum.x, sum.y);
+          w.y = pack_bf16x2(sum.z, sum.w);
+          *reinterpret_cast<uint2 *>(out + c * 128 + 4 * lane) = w;
+        }
     }
   }
   tc_fence_before();
