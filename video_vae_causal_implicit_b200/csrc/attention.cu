@@ -72,8 +72,8 @@ struct Ranges {
 
 // The tokens of frames first .. last (none if last < first), and of the
 // sinks up to frame `last_sink`, in a cache of the given shape.
-__device__ __forceinline__ Ranges token_ranges(const CacheShape &c, int first, int last,
-                                               int last_sink) {
+__device__ __forceinline__ Ranges token_ranges(const CacheShape &c, const FastDiv &by_ring,
+                                               int first, int last, int last_sink) {
   Ranges r;
   const int f = c.frame;
   const int ns = last_sink < 0 ? 0 : (last_sink >= c.sinks ? c.sinks : last_sink + 1);
@@ -94,7 +94,8 @@ __device__ __forceinline__ Ranges token_ranges(const CacheShape &c, int first, i
         r.lo[2] = c.sinks * f;
         r.hi[2] = (c.sinks + c.ring) * f;
       } else {
-        const int s0 = (first - c.sinks) % c.ring, e = s0 + count;
+        const int from = first - c.sinks;
+        const int s0 = from - by_ring.quotient(from) * c.ring, e = s0 + count;
         r.lo[2] = (c.sinks + s0) * f;
         r.hi[2] = (c.sinks + (e < c.ring ? e : c.ring)) * f;
         if (e > c.ring) {  // wrapped around
@@ -256,6 +257,64 @@ __device__ __forceinline__ void tmem_ld_all64(uint32_t taddr, uint32_t *r) {
       : "r"(taddr + 0), "r"(taddr + 32)
       : "memory");
 }
+// The rows rank, rank + split, ... of a split's `rows`: a warp takes 8 / KS
+// rows at a time (KS >= split), a lane four channels of each piece of 128, and
+// every rank's part is on its way before the first is added, in rank order.
+template <int KS, int PIECES>
+__device__ __forceinline__ void finish_rows(const AttnArgs &p, int rank, int rows,
+                                            uint32_t smem_base, int pitch, int seq, int kv_head,
+                                            int tok0) {
+  constexpr int kBatch = 8 / KS;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int warps = static_cast<int>(blockDim.x) / 32;
+  const int tile_rows = p.tok_tile * p.group;  // used rows of a row tile
+  const int step = p.split * warps;
+  for (int row0 = rank + p.split * warp; row0 < rows; row0 += step * kBatch) {
+    float4 v[kBatch][PIECES][KS];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int row = row0 + b * step;
+      if (row >= rows) continue;
+      const int r = row >= tile_rows ? row - tile_rows + kRows : row;  // (two row tiles at most)
+      const uint32_t at = smem_base + static_cast<uint32_t>(r * pitch + 4 * lane) * 4u;
+#pragma unroll
+      for (int c = 0; c < PIECES; ++c)
+        if (c * 128 + 4 * lane < p.c.d) {
+#pragma unroll
+          for (int k = 0; k < KS; ++k)
+            if (k < p.split) v[b][c][k] = ld_cluster_f32x4(mapa_shared(at + c * 512u, k));
+        }
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int row = row0 + b * step;
+      if (row >= rows) continue;
+      const int tk = p.by_group.quotient(row);
+      __nv_bfloat16 *out = p.o + static_cast<long long>(seq) * p.o_seq +
+                           static_cast<long long>(tok0 + tk) * p.o_tok +
+                           static_cast<long long>(kv_head * p.group + row - tk * p.group) *
+                               p.o_head;
+#pragma unroll
+      for (int c = 0; c < PIECES; ++c)
+        if (c * 128 + 4 * lane < p.c.d) {
+          float4 sum = v[b][c][0];
+#pragma unroll
+          for (int k = 1; k < KS; ++k)
+            if (k < p.split) {
+              sum.x += v[b][c][k].x;
+              sum.y += v[b][c][k].y;
+              sum.z += v[b][c][k].z;
+              sum.w += v[b][c][k].w;
+            }
+          uint2 w;
+          w.x = pack_bf16x2(sum.x, sum.y);
+          w.y = pack_bf16x2(sum.z, sum.w);
+          *reinterpret_cast<uint2 *>(out + c * 128 + 4 * lane) = w;
+        }
+    }
+  }
+}
+
 // NQ row tiles of 128, key tiles of KT tokens.  Every row tile has two slots
 // for its scores, so that the scores of the next key tile are there when the
 // softmax of one ends.
@@ -334,18 +393,20 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
   // one sequence and kv head.
   int kv_head, seq, tok0, tok_end, base;
   {
-    int i = static_cast<int>(blockIdx.x) / split;
-    kv_head = i % cs.kv_heads;
-    i /= cs.kv_heads;
-    seq = i % cs.n;
+    int i = p.by_split.quotient(static_cast<int>(blockIdx.x));
+    int up = p.by_kv.quotient(i);
+    kv_head = i - up * cs.kv_heads;
+    i = up;
+    up = p.by_n.quotient(i);
+    seq = i - up * cs.n;
     // the last query tiles see the most keys: first
-    const int tile = p.q_tiles - 1 - i / cs.n;
+    const int tile = p.q_tiles - 1 - up;
     int chunk, all;
     lengths(cs, seq, chunk, all);
     base = all - chunk;  // frame of query token 0 (negative: sees nothing)
     tok_end = chunk * cs.frame;
     if (p.tiles_frame > 0) {  // tiles that end with their frame
-      const int f = tile / p.tiles_frame;
+      const int f = p.by_tiles_frame.quotient(tile);
       tok0 = f * cs.frame + (tile - f * p.tiles_frame) * (NQ * p.tok_tile);
       tok_end = min(tok_end, (f + 1) * cs.frame);
     } else {
@@ -355,14 +416,15 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
   }
   const int reach = p.window > 0 ? p.window - 1 : INT32_MAX;  // frames back
   auto back = [&](int qf) { return qf > reach ? qf - reach : 0; };
-  const int qf0 = base + tok0 / cs.frame;
-  const int qf1 = tok_end > tok0 ? base + (tok_end - 1) / cs.frame : -1;
+  const int qf0 = base + p.by_frame.quotient(tok0);
+  const int qf1 = tok_end > tok0 ? base + p.by_frame.quotient(tok_end - 1) : -1;
   // keys that some query of the CTA sees, and keys that all of them see
-  const Ranges any = token_ranges(cs, back(qf0), qf1, qf1);
-  const Ranges every = token_ranges(cs, back(qf1), qf1 < 0 ? -1 : qf0, qf1 < 0 ? -1 : qf0);
+  const Ranges any = token_ranges(cs, p.by_ring, back(qf0), qf1, qf1);
+  const Ranges every = token_ranges(cs, p.by_ring, back(qf1), qf1 < 0 ? -1 : qf0, qf1 < 0 ? -1 : qf0);
   const TileList<KT> tiles(any);
-  const int j0 = static_cast<int>(static_cast<long long>(tiles.total) * rank / split);
-  const int nj = static_cast<int>(static_cast<long long>(tiles.total) * (rank + 1) / split) - j0;
+  // (at most 2^25 tiles of at most 8 ranks)
+  const int j0 = p.by_split.quotient(tiles.total * rank);
+  const int nj = p.by_split.quotient(tiles.total * (rank + 1)) - j0;
   bool ok = true;
 
   // (registers move in the branches: code after a common point gets the
@@ -525,13 +587,14 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
     const int quarter = warp % 4;               // the tensor-memory lanes it may read
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const int r = quarter * 32 + lane;  // its row of the tile
-    const int tok = tok0 + wg * p.tok_tile + r / p.group;
-    const int head = kv_head * p.group + r % p.group;
+    const int tok_r = p.by_group.quotient(r);
+    const int tok = tok0 + wg * p.tok_tile + tok_r;
+    const int head = kv_head * p.group + r - tok_r * p.group;
     const bool live = r < p.tok_tile * p.group && tok < tok_end;
     Ranges mine;
     {
-      const int qf = live ? base + tok / cs.frame : -1;
-      mine = token_ranges(cs, back(qf), qf, qf);
+      const int qf = live ? base + p.by_frame.quotient(tok) : -1;
+      mine = token_ranges(cs, p.by_ring, back(qf), qf, qf);
     }
     const float c = p.scale_log2;
     float m = -INFINITY, l = 0.f;  // the maximum that p is relative to, and sum of p
@@ -724,20 +787,25 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
     // its shared memory (the keys are done with), and finishes the rows rank,
     // rank + split, ...
     const int pitch = cs.d + 4;  // floats: rows start in different banks
-    constexpr int kPieces = (CH + 1) / 2;
     float *part = reinterpret_cast<float *>(smem);
     const int tile_rows = p.tok_tile * p.group;  // used rows of a row tile
     if (warp >= kFirstRowWarp) {
       const int wg = (warp - kFirstRowWarp) / 4;
       const int r = (warp % 4) * 32 + lane;
       const uint32_t ml = smem_u32(row_ml) + 8u * (wg * kRows + r);
+      float2 of[8];  // every rank's (maximum, sum)
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < split) of[k] = ld_cluster_f32x2(mapa_shared(ml, k));
       float top = -INFINITY;
-      for (int k = 0; k < split; ++k) top = fmaxf(top, ld_cluster_f32x2(mapa_shared(ml, k)).x);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < split) top = fmaxf(top, of[k].x);
       float all = 0.f;
-      for (int k = 0; k < split; ++k) {
-        const float2 v = ld_cluster_f32x2(mapa_shared(ml, k));
-        if (v.x != -INFINITY) all += v.y * exp2_fast((v.x - top) * p.scale_log2);
-      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < split && of[k].x != -INFINITY)
+          all += of[k].y * exp2_fast((of[k].x - top) * p.scale_log2);
       const float2 me = row_ml[wg * kRows + r];
       float f = 0.f;
       if (me.x != -INFINITY && (all > 0.f || all != all))
@@ -769,44 +837,10 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
     __syncwarp();
     cluster_sync();
     griddep_wait();
-    // a warp a row, a lane four channels at a time, every rank's on their way
-    // before the first is added
     const int rows = max(0, tok_end - tok0) * p.group;  // of all row tiles
-    const int warps = static_cast<int>(blockDim.x) / 32;
-    for (int row = rank + split * warp; row < rows; row += split * warps) {
-      const int q = row / tile_rows, r = row - q * tile_rows;
-      const int tk = row / p.group;
-      __nv_bfloat16 *out = p.o + static_cast<long long>(seq) * p.o_seq +
-                           static_cast<long long>(tok0 + tk) * p.o_tok +
-                           static_cast<long long>(kv_head * p.group + row - tk * p.group) * p.o_head;
-      const uint32_t at =
-          smem_base + static_cast<uint32_t>((q * kRows + r) * pitch + 4 * lane) * 4u;
-      float4 v[kPieces][8];
-#pragma unroll
-      for (int c = 0; c < kPieces; ++c)
-        if (c * 128 + 4 * lane < cs.d) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (k < split) v[c][k] = ld_cluster_f32x4(mapa_shared(at + c * 512u, k));
-        }
-#pragma unroll
-      for (int c = 0; c < kPieces; ++c)
-        if (c * 128 + 4 * lane < cs.d) {
-          float4 sum = v[c][0];
-#pragma unroll
-          for (int k = 1; k < 8; ++k)
-            if (k < split) {
-              sum.x += v[c][k].x;
-              sum.y += v[c][k].y;
-              sum.z += v[c][k].z;
-              sum.w += v[c][k].w;
-            }
-          uint2 w;
-          w.x = pack_bf16x2(sum.x, sum.y);
-          w.y = pack_bf16x2(sum.z, sum.w);
-          *reinterpret_cast<uint2 *>(out + c * 128 + 4 * lane) = w;
-        }
-    }
+    if (split <= 2) finish_rows<2, (CH + 1) / 2>(p, rank, rows, smem_base, pitch, seq, kv_head, tok0);
+    else if (split <= 4) finish_rows<4, (CH + 1) / 2>(p, rank, rows, smem_base, pitch, seq, kv_head, tok0);
+    else finish_rows<8, (CH + 1) / 2>(p, rank, rows, smem_base, pitch, seq, kv_head, tok0);
   }
   tc_fence_before();
   __syncthreads();
@@ -1037,6 +1071,13 @@ cudaError_t launch_attention(AttnArgs a, const void *q, const Strides &sq, const
   if (!pick) return cudaErrorInvalidValue;
   const int kt = pick->kt;
   a.q_tiles = static_cast<int>(q_tiles);
+  a.by_frame = FastDiv(static_cast<uint32_t>(c.frame));
+  a.by_group = FastDiv(static_cast<uint32_t>(a.group));
+  a.by_kv = FastDiv(static_cast<uint32_t>(c.kv_heads));
+  a.by_n = FastDiv(static_cast<uint32_t>(c.n));
+  a.by_split = FastDiv(static_cast<uint32_t>(a.split));
+  a.by_ring = FastDiv(static_cast<uint32_t>(c.ring > 0 ? c.ring : 1));
+  a.by_tiles_frame = FastDiv(static_cast<uint32_t>(a.tiles_frame > 0 ? a.tiles_frame : 1));
   const long long grid = q_tiles * heads * a.split;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
   CUtensorMap mq, mk, mv;

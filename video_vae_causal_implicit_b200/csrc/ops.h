@@ -71,6 +71,24 @@ struct LinearArgs {
 cudaError_t launch_linear(LinearArgs a, const void *x, long long ldx, const void *w,
                           long long ldw, bool fp8, int sm_count, cudaStream_t stream);
 
+// x / d for 0 <= x < 2^31 by a multiplication (Granlund and Montgomery,
+// "Division by invariant integers using multiplication"): with l = ceil(log2
+// d) and mul = floor(2^32 (2^l - d) / d) + 1 the quotient is (x + (x mul >> 32)) >> l.
+struct FastDiv {
+  uint32_t d, mul, shift;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t div) : d(div), mul(1), shift(0) {
+    while ((1ull << shift) < div) ++shift;
+    mul = static_cast<uint32_t>(((1ull << 32) * ((1ull << shift) - div)) / div + 1);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ int quotient(int x) const {
+    return static_cast<int>((static_cast<uint32_t>(x) + __umulhi(static_cast<uint32_t>(x), mul)) >>
+                            shift);
+  }
+#endif
+};
+
 // Which frame of a sequence a cache slot holds: slot s < sinks frame s; the
 // later slots frame s (ring 0), or cyclically the last `ring` frames.
 struct CacheShape {
@@ -92,6 +110,7 @@ struct AttnArgs {
   // set by launch_attention; tiles_frame: query tiles of a frame, 0 where tiles
   // cross frames
   int split, q_tiles, tiles_frame;
+  FastDiv by_frame, by_group, by_kv, by_n, by_split, by_ring, by_tiles_frame;
 };
 struct Strides {
   long long seq, tok, head;  // in elements
