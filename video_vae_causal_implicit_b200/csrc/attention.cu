@@ -46,7 +46,6 @@ constexpr uint32_t kQChunk = kRows * 128;         // 64 channels of them
 constexpr size_t kSmemMost = 227 * 1024;
 constexpr uint64_t kDrainNs = 1000000000ull;
 constexpr float kGrow = 8.f;                      // log2 of the growth that p may take
-constexpr uint32_t kTmemCols = 512;
 
 // Token ranges of the cache, in slot order, and the tiles that hold them.
 struct Ranges {
@@ -159,7 +158,7 @@ __device__ __forceinline__ void lengths(const CacheShape &c, int seq, int &chunk
 // one barrier each: whole tiles where several fit beside Q, single chunks for
 // wide heads (a slot is then free, and its next load on its way, as soon as
 // four products have read it).  P V runs in steps of PC chunks (N = 64 PC).
-template <int NQ, int KT, int CH>
+template <int NQ, int KT, int CH, int OCC>
 struct Shape {
   static constexpr int GC = CH <= 2 ? CH : 1;
   static constexpr int NG = CH / GC;
@@ -175,14 +174,17 @@ struct Shape {
   static constexpr int stages() {
     int st = 24;
     // (whole steps of P V side by side)
-    while (kQ + st * kGroup + rest(st) > kSmemMost || st % (PC / GC) != 0) --st;
+    while (kQ + st * kGroup + rest(st) > kSmemMost / OCC - (OCC > 1 ? 1024 : 0) ||
+           st % (PC / GC) != 0)
+      --st;
     return st;
   }
   static constexpr int kStages = stages();
   static constexpr uint32_t kBars = kQ + kStages * kGroup;
   static constexpr uint32_t kSmem = kBars + rest(kStages);
   // tensor memory: two slots of scores and the output per row tile
-  static_assert(2 * NQ * KT + NQ * 64 * CH <= 512, "tensor memory columns");
+  static constexpr uint32_t kTmemCols = 512 / OCC;
+  static_assert(2 * NQ * KT + NQ * 64 * CH <= static_cast<int>(kTmemCols), "tensor memory columns");
   // a value tile, the key tile two ahead and the value tile before fit at once
   static_assert(kStages >= 3 * NG || (NQ == 1 && kStages >= 2 * NG), "ring depth");
   // the parts of a split: rows of d + 4 floats
@@ -325,12 +327,12 @@ __device__ __forceinline__ void finish_rows(const AttnArgs &p, int rank, int row
 // product.  One thread cannot issue them that fast (a barrier wait costs it
 // some 130 cycles, a product 40), so two warps do: one per row tile, or one
 // per kind.
-template <int NQ, int KT, int CH>
-__global__ void __launch_bounds__(attn_threads(NQ), 1)
+template <int NQ, int KT, int CH, int OCC>
+__global__ void __launch_bounds__(attn_threads(NQ), OCC)
     attn_kernel(const __grid_constant__ CUtensorMap map_q,
                 const __grid_constant__ CUtensorMap map_k,
                 const __grid_constant__ CUtensorMap map_v, const AttnArgs p) {
-  using S = Shape<NQ, KT, CH>;
+  using S = Shape<NQ, KT, CH, OCC>;
   constexpr int GC = S::GC, NG = S::NG, stages = S::kStages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -371,7 +373,7 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
     prefetch_tmap(&map_v);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_alloc(tmem_slot, S::kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -848,7 +850,7 @@ __global__ void __launch_bounds__(attn_threads(NQ), 1)
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc(tmem, S::kTmemCols);
   }
 }
 
@@ -905,20 +907,22 @@ using AttnKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensor
 // zero-padded; `step`: cycles of a key tile, measured in the loop.
 struct Variant {
   AttnKernel kernel;
-  int nq, kt, d_above, d_most, threads;
+  int nq, kt, occ, d_above, d_most, threads;
   uint32_t smem;
   double step;
 };
-constexpr int kVariants = 6;
-template <int NQ, int KT, int CH>
+constexpr int kVariants = 8;
+template <int NQ, int KT, int CH, int OCC>
 Variant variant(int d_above, double step) {
-  return Variant{attn_kernel<NQ, KT, CH>, NQ, KT, d_above, 64 * CH, attn_threads(NQ),
-                 Shape<NQ, KT, CH>::kSmem, step};
+  return Variant{attn_kernel<NQ, KT, CH, OCC>, NQ, KT, OCC, d_above, 64 * CH,
+                 attn_threads(NQ), Shape<NQ, KT, CH, OCC>::kSmem, step};
 }
 const Variant (&variants())[kVariants] {
   static const Variant v[kVariants] = {
-      variant<2, 64, 1>(0, 1600.0),    variant<2, 64, 2>(64, 1700.0), variant<1, 128, 1>(0, 2000.0),
-      variant<1, 128, 2>(64, 2600.0), variant<1, 64, 4>(128, 1800.0), variant<1, 64, 6>(256, 2400.0)};
+      variant<2, 64, 1, 1>(0, 1700.0),  variant<2, 64, 2, 1>(64, 1780.0),
+      variant<1, 64, 1, 2>(0, 1750.0),  variant<1, 64, 2, 2>(64, 1850.0),
+      variant<1, 128, 1, 1>(0, 2000.0), variant<1, 128, 2, 1>(64, 2100.0),
+      variant<1, 64, 4, 1>(128, 1800.0), variant<1, 64, 6, 1>(256, 2400.0)};
   return v;
 }
 
@@ -966,7 +970,7 @@ cudaError_t prepare_kernels(int sm_count, const Prepared **out) {
                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                static_cast<int>(v.smem));
       if (e != cudaSuccess) return e;
-      p.fit[i][1] = sm_count;  // (one CTA per SM)
+      p.fit[i][1] = sm_count * v.occ;
       for (int split = 2; split <= 8; ++split) {
         cudaLaunchAttribute attr[2];
         const cudaLaunchConfig_t cfg =
@@ -1032,10 +1036,11 @@ cudaError_t launch_attention(AttnArgs a, const void *q, const Strides &sq, const
   };
   const long long have = c.k_frames || c.ring > 0 ? c.slots : c.total;  // frames there are
   // Candidates: two row tiles a CTA (d <= 128: a key tile is read once for
-  // both, and one's softmax runs under the other's products) or one, keys
-  // split over 1 to 8 CTAs of a cluster; the least time by the cycles that
-  // the steps of a key tile, a CTA's start and end, and the joining of the
-  // parts were measured to take, over whole waves of what fits at once.
+  // both, and one's softmax runs under the other's products), one, or one and
+  // two CTAs an SM; keys split over 1 to 8 CTAs of a cluster.  The least time
+  // by the cycles that a key tile's steps, a CTA's start and end, and the
+  // joining of the parts were measured to take (d = 64 to 384, 1 to 8190
+  // queries, 500 to 20000 keys), over whole waves of what fits at once.
   double best = 1e300;
   long long q_tiles = 0;
   const Variant *pick = nullptr;
@@ -1051,14 +1056,16 @@ cudaError_t launch_attention(AttnArgs a, const void *q, const Strides &sq, const
     const long long frames = seen + (span < c.t ? span : c.t) - 1;
     const long long keys = (frames < have ? frames : have) * c.frame;
     const double steps = static_cast<double>((keys + v.kt - 1) / v.kt);
-    for (int split = 1; split <= 8 && (split == 1 || split * 2 <= steps); ++split) {
+    for (int split = 1; split <= 8 && split <= steps; ++split) {
       const int fit = prepared->fit[&v - variants()][split];
       if (fit < 1) continue;
       // (a few waves are whole ones; the last of many overlaps the others')
       const double parts = static_cast<double>(tiles * heads) / fit;
       const double waves = parts < 4.0 ? std::ceil(parts) : parts + 0.5;
-      const double t = waves * (std::ceil(steps / split) * v.step + 7000.0 +
-                                (split > 1 ? 3000.0 + 8.0 * v.nq * c.d : 0.0));
+      // (alone on its SM a CTA of a pair steps faster)
+      const double step = v.occ == 2 && tiles * heads * split <= sm_count ? 0.85 * v.step : v.step;
+      const double join = split > 1 ? 3000.0 + 30.0 * v.nq * c.d : 0.0;
+      const double t = waves * (std::ceil(steps / split) * step + 7000.0 + 20.0 * c.d + join);
       if (t < best) {
         best = t;
         pick = &v;
