@@ -1,0 +1,69 @@
+"""Bounded waits of the transformer operators, without a GPU fault: a child
+process runs with a 1 microsecond wait limit (CC3D_WAIT_LIMIT_US=1), so that
+the pipelines' first real waits run out.  Each kernel has to record it, drain
+its own copies and products, free tensor memory and return (the barriers
+between an attention kernel's warps included, and the clusters that split
+keys or K); the host sees CC3D_ERR_TIMEOUT once and the context stays
+usable.  (One CTA per tile, not a CTA pair: see the conv's test.)"""
+import json
+import os
+import subprocess
+import sys
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+CHILD = r"""
+import json, sys, torch
+sys.path.insert(0, %r)
+from video_vae_causal_implicit_b200 import cc3d
+out = {}
+b16 = dict(device='cuda', dtype=torch.bfloat16)
+
+def status(name):
+    out[name] = [cc3d.cc3d_sync_status(cc3d._stream()), cc3d.cc3d_sync_status(cc3d._stream())]
+
+def linear(name, m, n, k, residual):
+    x, w = torch.randn(m, k, **b16), torch.randn(n, k, **b16)
+    y, r = torch.empty(m, n, **b16), torch.randn(m, n, **b16)
+    torch.cuda.synchronize()
+    cc3d.linear(x, w, y, residual=r if residual else None)
+    status(name)
+
+linear('linear', 1560, 1152, 384, False)
+linear('linear residual', 1560, 1152, 384, True)
+linear('linear split', 1, 512, 4096, False)
+
+def attention(name, n, t, total, heads, kv, d, **kw):
+    q = torch.randn(n, t, heads, d, **b16)
+    k, v = torch.randn(n, total, kv, d, **b16), torch.randn(n, total, kv, d, **b16)
+    o = torch.empty_like(q)
+    torch.cuda.synchronize()
+    cc3d.attention(q, k, v, o, total=total, **kw)
+    status(name)
+
+attention('attention two tiles', 1, 2048, 2048, 32, 32, 128)   # turns between the row tiles
+attention('attention split', 1, 1, 4000, 8, 2, 128)            # keys over a cluster
+attention('attention wide', 1, 300, 300, 1, 1, 384)
+attention('attention two CTAs', 16, 64, 1500, 16, 16, 64, window=300)
+torch.cuda.synchronize()
+out['torch_after'] = (torch.arange(1024, device='cuda', dtype=torch.float32) * 2).sum().item()
+print('RESULT ' + json.dumps(out))
+""" % ROOT
+
+
+def test_bounded_waits_report_timeout_and_leave_context_usable():
+    env = dict(os.environ, CC3D_WAIT_LIMIT_US="1")
+    proc = subprocess.run([sys.executable, "-c", CHILD], env=env, capture_output=True, text=True,
+                          timeout=300)
+    assert proc.returncode == 0, proc.stderr[-3000:]
+    line = [l for l in proc.stdout.splitlines() if l.startswith("RESULT ")][-1]
+    res = json.loads(line[len("RESULT "):])
+    TIMEOUT, OK = 7, 0
+    assert res.pop("torch_after") == float(sum(range(1024)) * 2)
+    for name, (first, second) in res.items():
+        assert first == TIMEOUT, name
+        assert second == OK, name  # reading the status clears it

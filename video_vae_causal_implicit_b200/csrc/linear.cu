@@ -210,11 +210,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (++s == p.stages) { s = 0; ph ^= 1; }
         }
       }
-      // every load lands before the CTA may exit (the leader's barriers count
-      // both CTAs' loads; the follower waits at the final cluster barrier)
-      if (!leader) used = 0;
+      // Every load lands before the CTA may exit.  A pair's loads complete on
+      // the leader's barriers, so its follower waits until the products have
+      // read them, and where they never do (the leader gave up), long enough
+      // for a load that is under way.
+      bool landed = true;
       for (int i = 0; i < p.stages; ++i)
-        if (used >> i & 1u) mbar_wait_bounded(&full[i], par >> i & 1u, kDrainNs, nullptr, 0);
+        if (used >> i & 1u)
+          landed &= leader ? mbar_wait_bounded(&full[i], par >> i & 1u, kDrainNs, nullptr, 0)
+                           : mbar_wait_bounded(&empty[i], par >> i & 1u, p.wait_limit_ns, nullptr, 0);
+      if (!leader && !landed)
+        for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 1000000ull;) {
+        }
     }
   } else if (warp == 1) {
     if (leader && elect_one()) {
