@@ -477,6 +477,7 @@ __global__ void __launch_bounds__(attn_threads(NQ), OCC)
     // ------------------------------ products ------------------------------------
     if constexpr (NQ == 2) regs_fewer<kRegsFew>();
     if (nj > 0 && elect_one()) {
+      griddep_wait();  // (a wait's limit does not count the kernels before)
       constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, KT);
       constexpr uint32_t idesc_o = idesc_bf16_f32_bt(kRows, 64 * S::PC);
       const uint64_t qd = smem_desc_sw128(smem_base, 1024u);
@@ -585,6 +586,7 @@ __global__ void __launch_bounds__(attn_threads(NQ), OCC)
   } else if (warp >= kFirstRowWarp) {
     // ------------------------------ softmax, output ------------------------------
     if constexpr (NQ == 2) regs_more<kRegsMany>();
+    griddep_wait();
     const int wg = (warp - kFirstRowWarp) / 4;  // this warp's row tile
     const int quarter = warp % 4;               // the tensor-memory lanes it may read
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
@@ -740,7 +742,6 @@ __global__ void __launch_bounds__(attn_threads(NQ), OCC)
       const float inv = (l > 0.f || l != l) ? 1.f / l : 0.f;
       const uint32_t o = o_col + wg * o_cols + lanes;
       uint8_t *stage = smem + static_cast<uint32_t>(wg * CH) * kQChunk + quarter * 4096u;
-      griddep_wait();
 #pragma unroll 1
       for (int i = 0; i < cs.d; i += 64) {
 #pragma unroll

@@ -225,6 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     if (leader && elect_one()) {
+      griddep_wait();  // (a wait's limit does not count the kernels before)
       const uint32_t idesc = FP8 ? idesc_e4m3_f32(kRowsPerTile, p.nt)
                                  : idesc_bf16_f32(kRowsPerTile, p.nt);
       const uint64_t a0 = smem_desc_sw128(smem_base, 1024u);
