@@ -427,10 +427,16 @@ typedef enum {
  * q; q needs exactly one of scales and scale >= 1e-36 (scale is ignored
  * without q), else CC3D_ERR_INVALID_ARG.  Any other overlap of an output
  * with an argument is CC3D_ERR_ALIAS.  rows = 0 does nothing. */
-cc3d_status cc3d_add_rms_norm(const void *x, const void *residual, const float *gamma,
-                              const float *beta, long long rows, int c, float eps, int silu,
-                              void *h, void *y, void *q, float *scales, float scale,
-                              void *stream);
+typedef struct {
+  const void *x, *residual;
+  const float *gamma, *beta;
+  void *h, *y, *q;
+  float *scales;
+  long long rows;
+  int c, silu;
+  float eps, scale;
+} cc3d_add_norm_call;
+cc3d_status cc3d_add_rms_norm(const cc3d_add_norm_call *call, void *stream);
 
 /* Matrix product with its epilogue, fp32 accumulation, rounded once:
  *   y[m,n] = bf16(act(s_x[m] * s_w[n] * sum_k x[m,k] weight[n,k] + bias[n]) + residual[m,n])
@@ -446,11 +452,20 @@ cc3d_status cc3d_add_rms_norm(const void *x, const void *residual, const float *
  * multiples of 8 (bf16) or 16 (E4M3); n, ldy, ldr multiples of 8; m, n, k and
  * row distances at most 2^30, else CC3D_ERR_UNSUPPORTED.  m = 0 does nothing.
  * One kernel launch; the same arguments give the same bytes on every call. */
-cc3d_status cc3d_linear(const void *x, long long ldx, const void *weight, long long ldw,
-                        const float *bias, const void *residual, long long ldr, void *y,
-                        long long ldy, long long m, int n, int k, cc3d_dtype dtype, cc3d_act act,
-                        const float *x_scales, float x_scale, const float *w_scales,
-                        void *stream);
+typedef struct {
+  const void *x, *weight;
+  const float *bias;
+  const void *residual;
+  void *y;
+  const float *x_scales, *w_scales;
+  long long ldx, ldw, ldr, ldy; /* ldr is ignored without a residual */
+  long long m;
+  int n, k;
+  cc3d_dtype dtype;
+  cc3d_act act;
+  float x_scale;
+} cc3d_linear_call;
+cc3d_status cc3d_linear(const cc3d_linear_call *call, void *stream);
 
 /* Attention in a sliding window of frames, with sink frames (bf16, fp32
  * softmax).  A frame is `frame` consecutive tokens.  A query of frame i sees

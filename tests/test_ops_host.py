@@ -1,8 +1,6 @@
 """Refusals of the transformer operators' entry points: every check runs on
 the host before anything is launched, so these need no GPU (the addresses
 are never followed)."""
-import ctypes
-
 import pytest
 
 from video_vae_causal_implicit_b200 import build as cbuild
@@ -15,17 +13,17 @@ def lib():
     return cc3d.lib()
 
 
-def P(a):
-    return None if a is None else ctypes.c_void_p(a)
+# the calls' fields, in the header's order (and names)
+NORM = "x residual gamma beta h y q scales rows c silu eps scale".split()
+LINEAR = ("x weight bias residual y x_scales w_scales ldx ldw ldr ldy m n k dtype act "
+          "x_scale").split()
 
 
 def norm(lib, **kw):
     a = dict(x=0x100000, residual=None, gamma=0x1000, beta=None, rows=4, c=64, eps=1e-6, silu=0,
              h=None, y=0x200000, q=None, scales=None, scale=0.0)
     a.update(kw)
-    return lib.cc3d_add_rms_norm(P(a["x"]), P(a["residual"]), P(a["gamma"]), P(a["beta"]),
-                                 a["rows"], a["c"], a["eps"], a["silu"], P(a["h"]), P(a["y"]),
-                                 P(a["q"]), P(a["scales"]), a["scale"], None)
+    return lib.cc3d_add_rms_norm(cc3d._NORM_CALL.pack(*(a[k] or 0 for k in NORM)), None)
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -56,40 +54,40 @@ def test_add_rms_norm_refusals(lib, kw, status):
 
 
 def linear(lib, **kw):
-    a = dict(x=0x1000000, ldx=64, w=0x2000000, ldw=64, bias=None, res=None, ldr=0, y=0x3000000,
-             ldy=32, m=4, n=32, k=64, dtype=cc3d.BF16, act=0, xs=None, x_scale=0.0, ws=None)
+    a = dict(x=0x1000000, ldx=64, weight=0x2000000, ldw=64, bias=None, residual=None, ldr=0,
+             y=0x3000000, ldy=32, m=4, n=32, k=64, dtype=cc3d.BF16, act=0, x_scales=None,
+             x_scale=0.0, w_scales=None)
     a.update(kw)
-    return lib.cc3d_linear(P(a["x"]), a["ldx"], P(a["w"]), a["ldw"], P(a["bias"]), P(a["res"]),
-                           a["ldr"], P(a["y"]), a["ldy"], a["m"], a["n"], a["k"], a["dtype"],
-                           a["act"], P(a["xs"]), a["x_scale"], P(a["ws"]), None)
+    assert set(kw) <= set(a)
+    return lib.cc3d_linear(cc3d._LINEAR_CALL.pack(*(a[k] or 0 for k in LINEAR)), None)
 
 
-E4M3 = dict(dtype=cc3d.FP8_E4M3, ws=0x5000000, x_scale=0.5)
+E4M3 = dict(dtype=cc3d.FP8_E4M3, w_scales=0x5000000, x_scale=0.5)
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(x=None), cc3d.ERR_INVALID_ARG), (dict(w=None), cc3d.ERR_INVALID_ARG),
+    (dict(x=None), cc3d.ERR_INVALID_ARG), (dict(weight=None), cc3d.ERR_INVALID_ARG),
     (dict(y=None), cc3d.ERR_INVALID_ARG), (dict(m=-1), cc3d.ERR_INVALID_ARG),
     (dict(n=0), cc3d.ERR_INVALID_ARG), (dict(k=0), cc3d.ERR_INVALID_ARG),
     (dict(ldx=56), cc3d.ERR_INVALID_ARG), (dict(ldw=0), cc3d.ERR_INVALID_ARG),
-    (dict(ldy=24), cc3d.ERR_INVALID_ARG), (dict(res=0x4000000, ldr=24), cc3d.ERR_INVALID_ARG),
+    (dict(ldy=24), cc3d.ERR_INVALID_ARG), (dict(residual=0x4000000, ldr=24), cc3d.ERR_INVALID_ARG),
     (dict(act=4), cc3d.ERR_INVALID_ARG), (dict(act=-1), cc3d.ERR_INVALID_ARG),
-    (dict(ws=0x5000000), cc3d.ERR_INVALID_ARG), (dict(x_scale=1.0), cc3d.ERR_INVALID_ARG),
-    (dict(E4M3, ws=None), cc3d.ERR_INVALID_ARG), (dict(E4M3, x_scale=0.0), cc3d.ERR_INVALID_ARG),
-    (dict(E4M3, xs=0x6000000), cc3d.ERR_INVALID_ARG),
+    (dict(w_scales=0x5000000), cc3d.ERR_INVALID_ARG), (dict(x_scale=1.0), cc3d.ERR_INVALID_ARG),
+    (dict(E4M3, w_scales=None), cc3d.ERR_INVALID_ARG), (dict(E4M3, x_scale=0.0), cc3d.ERR_INVALID_ARG),
+    (dict(E4M3, x_scales=0x6000000), cc3d.ERR_INVALID_ARG),
     (dict(E4M3, x_scale=float("nan")), cc3d.ERR_INVALID_ARG),
     (dict(dtype=cc3d.FP32), cc3d.ERR_UNSUPPORTED),
     (dict(k=60), cc3d.ERR_UNSUPPORTED), (dict(n=28), cc3d.ERR_UNSUPPORTED),
     (dict(ldx=68), cc3d.ERR_UNSUPPORTED), (dict(ldy=36), cc3d.ERR_UNSUPPORTED),
     (dict(E4M3, k=56), cc3d.ERR_UNSUPPORTED), (dict(E4M3, ldw=72), cc3d.ERR_UNSUPPORTED),
     (dict(m=(1 << 30) + 1), cc3d.ERR_UNSUPPORTED),
-    (dict(x=0x1000008), cc3d.ERR_ALIGNMENT), (dict(w=0x2000008), cc3d.ERR_ALIGNMENT),
+    (dict(x=0x1000008), cc3d.ERR_ALIGNMENT), (dict(weight=0x2000008), cc3d.ERR_ALIGNMENT),
     (dict(y=0x3000008), cc3d.ERR_ALIGNMENT), (dict(bias=0x4000004), cc3d.ERR_ALIGNMENT),
-    (dict(E4M3, ws=0x5000004), cc3d.ERR_ALIGNMENT),
-    (dict(E4M3, x_scale=0.0, xs=0x6000002), cc3d.ERR_ALIGNMENT),
+    (dict(E4M3, w_scales=0x5000004), cc3d.ERR_ALIGNMENT),
+    (dict(E4M3, x_scale=0.0, x_scales=0x6000002), cc3d.ERR_ALIGNMENT),
     (dict(y=0x1000000), cc3d.ERR_ALIAS), (dict(y=0x2000020), cc3d.ERR_ALIAS),
-    (dict(y=0x3000000, res=0x3000010, ldr=32), cc3d.ERR_ALIAS),
-    (dict(y=0x3000000, res=0x3000000, ldr=40), cc3d.ERR_ALIAS),
+    (dict(y=0x3000000, residual=0x3000010, ldr=32), cc3d.ERR_ALIAS),
+    (dict(y=0x3000000, residual=0x3000000, ldr=40), cc3d.ERR_ALIAS),
     (dict(bias=0x3000040), cc3d.ERR_ALIAS),
 ])
 def test_linear_refusals(lib, kw, status):
@@ -175,6 +173,8 @@ def test_kv_append_refusals(lib, kw, status):
 
 
 def test_null_calls_refused(lib):
+    assert lib.cc3d_add_rms_norm(None, None) == cc3d.ERR_INVALID_ARG
+    assert lib.cc3d_linear(None, None) == cc3d.ERR_INVALID_ARG
     assert lib.cc3d_attention(None, None) == cc3d.ERR_INVALID_ARG
     assert lib.cc3d_kv_append(None, None) == cc3d.ERR_INVALID_ARG
 
@@ -183,7 +183,8 @@ def test_packed_calls_have_the_headers_layout(tmp_path):
     """The wrappers' packed arguments against what the C compiler lays out."""
     import os
     import subprocess
-    names = {"cc3d_attn_call": ATTN, "cc3d_kv_call": KV}
+    names = {"cc3d_add_norm_call": NORM, "cc3d_linear_call": LINEAR, "cc3d_attn_call": ATTN,
+             "cc3d_kv_call": KV}
     body = "".join(f'printf("%zu ", sizeof({t}));' +
                    "".join(f'printf("%zu ", offsetof({t}, {f}));' for f in fs)
                    for t, fs in names.items())
@@ -194,7 +195,7 @@ def test_packed_calls_have_the_headers_layout(tmp_path):
     got = [int(v) for v in subprocess.run([str(tmp_path / "layout")], capture_output=True,
                                           text=True, check=True).stdout.split()]
     want = []
-    for s in (cc3d._ATTN_CALL, cc3d._KV_CALL):
+    for s in (cc3d._NORM_CALL, cc3d._LINEAR_CALL, cc3d._ATTN_CALL, cc3d._KV_CALL):
         codes = [(c, int(n or 1)) for n, c in __import__("re").findall(r"(\d*)([ifPq])", s.format)]
         want.append(s.size)
         at = 0

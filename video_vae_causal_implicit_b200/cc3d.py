@@ -62,7 +62,7 @@ class HostCall(ctypes.Structure):
 
 
 # name -> (restype, argtypes)
-_VP, _I, _LL, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float
+_VP, _I = ctypes.c_void_p, ctypes.c_int
 SIGNATURES = {
     "cc3d_plan_create": (_I, [ctypes.POINTER(Desc), ctypes.POINTER(_VP)]),
     "cc3d_plan_destroy": (_I, [_VP]),
@@ -85,9 +85,8 @@ SIGNATURES = {
     "cc3d_launch_count": (ctypes.c_uint64, []),
     "cc3d_forward_noalloc": (_I, [ctypes.POINTER(Desc), _VP, _I, _VP, _VP, _VP, _VP, _VP, _VP,
                                   _VP]),
-    "cc3d_add_rms_norm": (_I, [_VP, _VP, _VP, _VP, _LL, _I, _F, _I, _VP, _VP, _VP, _VP, _F, _VP]),
-    "cc3d_linear": (_I, [_VP, _LL, _VP, _LL, _VP, _VP, _LL, _VP, _LL, _LL, _I, _I, _I, _I, _VP, _F,
-                         _VP, _VP]),
+    "cc3d_add_rms_norm": (_I, [_VP, _VP]),
+    "cc3d_linear": (_I, [_VP, _VP]),
     "cc3d_attention": (_I, [_VP, _VP]),
     "cc3d_kv_append": (_I, [_VP, _VP]),
 }
@@ -353,6 +352,13 @@ def quantize_e4m3(x, scale, q, stream=None):
 # takes as long as its checks, so each is one expression and the reasons are
 # worked out only for a tensor that fails it.
 
+# The calls' argument structs as the C compiler lays them out (packing one is
+# a third of the time that as many ctypes arguments take)
+_NORM_CALL = struct.Struct("@8Pq2i2f")
+_LINEAR_CALL = struct.Struct("@7P5q4if4x")
+_ATTN_CALL = struct.Struct("@11if6P12q")
+_KV_CALL = struct.Struct("@9i6P12q")
+
 _torch = None  # torch and the types of the operators, on first use
 _B16 = _F32 = _B8 = _I32 = ()
 
@@ -428,9 +434,10 @@ def linear(x, weight, y, *, bias=None, residual=None, act=ACT_NONE, x_scales=Non
     py, ldy = _rows(y, "y", _B16, dev, (m, n))
     pr, ldr = _rows(residual, "residual", _B16, dev, (m, n)) if residual is not None else (0, 0)
     check((_lib or lib()).cc3d_linear(
-        px, ldx, pw, ldw, _flat(bias, "bias", _F32, dev, (n,)), pr, ldr, py, ldy, m, n, k,
-        FP8_E4M3 if fp8 else BF16, act, _flat(x_scales, "x_scales", _F32, dev, (m,)), x_scale,
-        _flat(w_scales, "w_scales", _F32, dev, (n,)), st), "cc3d_linear")
+        _LINEAR_CALL.pack(px, pw, _flat(bias, "bias", _F32, dev, (n,)), pr, py,
+                          _flat(x_scales, "x_scales", _F32, dev, (m,)),
+                          _flat(w_scales, "w_scales", _F32, dev, (n,)), ldx, ldw, ldr, ldy, m, n,
+                          k, FP8_E4M3 if fp8 else BF16, act, x_scale), st), "cc3d_linear")
     return y
 
 
@@ -445,16 +452,13 @@ def add_rms_norm(x, gamma, *, residual=None, beta=None, eps=0.0, silu=False, h=N
     c = shape[-1]
     rows = x.numel() // c if c else 0
     check((_lib or lib()).cc3d_add_rms_norm(
-        _flat(x, "x", _B16, dev, shape), _flat(residual, "residual", _B16, dev, shape),
-        _flat(gamma, "gamma", _F32, dev, (c,)), _flat(beta, "beta", _F32, dev, (c,)), rows, c, eps,
-        1 if silu else 0, _flat(h, "h", _B16, dev, shape), _flat(y, "y", _B16, dev, shape),
-        _flat(q, "q", _B8, dev, shape), _flat(scales, "scales", _F32, dev, shape[:-1]), scale,
-        st), "cc3d_add_rms_norm")
-
-
-# cc3d_attn_call and cc3d_kv_call as the C compiler lays them out
-_ATTN_CALL = struct.Struct("@11if6P12q")
-_KV_CALL = struct.Struct("@9i6P12q")
+        _NORM_CALL.pack(_flat(x, "x", _B16, dev, shape),
+                        _flat(residual, "residual", _B16, dev, shape),
+                        _flat(gamma, "gamma", _F32, dev, (c,)),
+                        _flat(beta, "beta", _F32, dev, (c,)), _flat(h, "h", _B16, dev, shape),
+                        _flat(y, "y", _B16, dev, shape), _flat(q, "q", _B8, dev, shape),
+                        _flat(scales, "scales", _F32, dev, shape[:-1]) if scales is not None else 0,
+                        rows, c, 1 if silu else 0, eps, scale), st), "cc3d_add_rms_norm")
 
 
 def _heads(t, name, dev, shape, frame):

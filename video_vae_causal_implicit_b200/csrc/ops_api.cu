@@ -130,10 +130,15 @@ using namespace cc3d;
 
 extern "C" {
 
-cc3d_status cc3d_add_rms_norm(const void *x, const void *residual, const float *gamma,
-                              const float *beta, long long rows, int c, float eps, int silu,
-                              void *h, void *y, void *q, float *scales, float scale,
-                              void *stream) {
+cc3d_status cc3d_add_rms_norm(const cc3d_add_norm_call *p, void *stream) {
+  if (!p) return CC3D_ERR_INVALID_ARG;
+  const void *x = p->x, *residual = p->residual;
+  const float *gamma = p->gamma, *beta = p->beta;
+  void *h = p->h, *y = p->y, *q = p->q;
+  float *scales = p->scales;
+  const long long rows = p->rows;
+  const int c = p->c;
+  const float eps = p->eps, scale = p->scale;
   if (rows < 0 || c < 1 || !(eps >= 0.f) || !std::isfinite(eps)) return CC3D_ERR_INVALID_ARG;
   if (rows == 0) return CC3D_OK;  // (such a call may come with null tensors)
   if (!x || !gamma || (!y && !q && !h)) return CC3D_ERR_INVALID_ARG;
@@ -181,15 +186,20 @@ cc3d_status cc3d_add_rms_norm(const void *x, const void *residual, const float *
   a.eps = eps;
   a.rows = rows;
   a.c = c;
-  a.silu = silu != 0;
+  a.silu = p->silu != 0;
   return status_of(launch_add_rms_norm(a, dev.sm_count, static_cast<cudaStream_t>(stream)));
 }
 
-cc3d_status cc3d_linear(const void *x, long long ldx, const void *weight, long long ldw,
-                        const float *bias, const void *residual, long long ldr, void *y,
-                        long long ldy, long long m, int n, int k, cc3d_dtype dtype, cc3d_act act,
-                        const float *x_scales, float x_scale, const float *w_scales,
-                        void *stream) {
+cc3d_status cc3d_linear(const cc3d_linear_call *p, void *stream) {
+  if (!p) return CC3D_ERR_INVALID_ARG;
+  const void *x = p->x, *weight = p->weight, *residual = p->residual;
+  const float *bias = p->bias, *x_scales = p->x_scales, *w_scales = p->w_scales;
+  void *y = p->y;
+  const long long ldx = p->ldx, ldw = p->ldw, ldr = p->ldr, ldy = p->ldy, m = p->m;
+  const int n = p->n, k = p->k;
+  const cc3d_dtype dtype = p->dtype;
+  const cc3d_act act = p->act;
+  const float x_scale = p->x_scale;
   // (a call without rows may come with null tensors)
   if ((m != 0 && (!x || !weight || !y)) || m < 0 || n < 1 || k < 1 || ldx < k || ldw < k || ldy < n ||
       (residual && ldr < n) || act < CC3D_ACT_NONE || act > CC3D_ACT_GELU_TANH)
