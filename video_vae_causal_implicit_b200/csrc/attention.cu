@@ -160,7 +160,7 @@ __device__ __forceinline__ void lengths(const CacheShape &c, int seq, int &chunk
 // four products have read it).  P V runs in steps of PC chunks (N = 64 PC).
 template <int NQ, int KT, int CH, int OCC>
 struct Shape {
-  static constexpr int GC = CH <= 2 ? CH : 1;
+  static constexpr int GC = CH <= 2 ? CH : 2;
   static constexpr int NG = CH / GC;
   static constexpr int PC = CH <= 2 ? CH : 2;
   static constexpr uint32_t kChunk = KT * 128u;
@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(attn_threads(NQ), OCC)
         const int tok = tiles.at(j0 + j) * KT;
 #pragma unroll 1
         for (int g = 0; g < NG && ok; ++g) {
-          if (!mbar_wait_bounded(&empty[s], ph ^ 1, p.wait_limit_ns, p.status, 30)) {
+          if (!mbar_wait_soon(&empty[s], ph ^ 1, p.wait_limit_ns, p.status, 30)) {
             ok = false;
             return;
           }
@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(attn_threads(NQ), OCC)
         if (x.slot >= stages) { x.slot -= stages; x.phase ^= 1; }
       };
       auto await = [&](uint64_t *bar, uint32_t parity, int site) {
-        if (ok && !mbar_wait_bounded(bar, parity, p.wait_limit_ns, p.status, site)) ok = false;
+        if (ok && !mbar_wait_soon(bar, parity, p.wait_limit_ns, p.status, site)) ok = false;
         return ok;
       };
       // S[q][slot] = Q[q] K^T, a group at a time as it arrives
@@ -605,8 +605,7 @@ __global__ void __launch_bounds__(attn_threads(NQ), OCC)
     // (every lane waits; the warp goes on as one)
     auto await = [&](uint64_t *bar, uint32_t parity, int site) {
       return __all_sync(0xffffffffu,
-                        mbar_test(bar, parity) ||
-                            mbar_wait_bounded(bar, parity, p.wait_limit_ns, p.status, site)) != 0;
+                        mbar_wait_soon(bar, parity, p.wait_limit_ns, p.status, site)) != 0;
     };
     // With two row tiles their exponentials take turns: the unit that
     // computes them is then busy with one tile's while the other's scores are

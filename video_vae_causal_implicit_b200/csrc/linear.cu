@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row_x = mt * kRowsPerTile + rank * kTileRows;
         const int row_w = nt * p.nt + rank * b_rows;
         for (int kc = 0; kc < nk; ++kc) {
-          if (!mbar_wait_bounded(&empty[s], ph ^ 1, p.wait_limit_ns, p.status, 20)) {
+          if (!mbar_wait_soon(&empty[s], ph ^ 1, p.wait_limit_ns, p.status, 20)) {
             ok = false;
             break;
           }
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t d = tmem_base + static_cast<uint32_t>(buf * p.nt);
         for (int kc = 0; kc < nk; ++kc) {
-          if (!mbar_wait_bounded(&full[s], ph, p.wait_limit_ns, p.status, 22)) {
+          if (!mbar_wait_soon(&full[s], ph, p.wait_limit_ns, p.status, 22)) {
             ok = false;
             break;
           }
@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(kSplitThreads)
       int s = 0;
       uint32_t ph = 0, used = 0, par = 0;
       for (int kc = k0; kc < k1; ++kc) {
-        if (!mbar_wait_bounded(&empty[s], ph ^ 1, p.wait_limit_ns, p.status, 24)) break;
+        if (!mbar_wait_soon(&empty[s], ph ^ 1, p.wait_limit_ns, p.status, 24)) break;
         mbar_arrive_expect_tx(&full[s], L.stage);
         used |= 1u << s;
         par = (par & ~(1u << s)) | (ph << s);
@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(kSplitThreads)
       int s = 0;
       uint32_t ph = 0;
       for (int kc = k0; kc < k1; ++kc) {
-        if (!mbar_wait_bounded(&full[s], ph, p.wait_limit_ns, p.status, 25)) break;
+        if (!mbar_wait_soon(&full[s], ph, p.wait_limit_ns, p.status, 25)) break;
         const uint64_t a = a0 + ((s * L.stage) >> 4), b = b0 + ((s * L.stage) >> 4);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {

@@ -106,6 +106,13 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity
   }
 }
 
+// The same wait for a phase that has mostly completed: the test that does not
+// suspend the thread answers some 90 cycles sooner than the one that may.
+__device__ __forceinline__ bool mbar_wait_soon(uint64_t *bar, uint32_t parity, uint64_t limit_ns,
+                                               int *status, int site) {
+  return mbar_test(bar, parity) || mbar_wait_bounded(bar, parity, limit_ns, status, site);
+}
+
 // ---- programmatic dependent launch ------------------------------------------------
 // Let the next kernel of the stream start (when it was launched with
 // programmatic stream serialization: on SMs this grid leaves free), and wait
