@@ -49,29 +49,42 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// act() of a pair in fp32: a / (1 + 2^z) with z = -a log2(e) for SiLU, and for
-// the tanh form of GELU, a (1 + tanh u) / 2 = a / (1 + exp(-2 u)), z = -2 u
-// log2(e), u = sqrt(2 / pi) (a + 0.044715 a^3).  The exponential and the
-// reciprocal are the hardware's (relative error about 2^-21), far below the
-// bf16 rounding of y.
-__device__ __forceinline__ uint64_t activate(uint64_t a, int act) {
-  if (act == CC3D_ACT_NONE) return a;
-  if (act == CC3D_ACT_GELU) {
-    const float2 v = unpair(a);
-    return pair_of(0.5f * v.x * erfcf(v.x * -0.70710678118654752f),
-                   0.5f * v.y * erfcf(v.y * -0.70710678118654752f));
-  }
-  uint64_t z;
-  if (act == CC3D_ACT_SILU) {
-    z = pair_mul(a, pair_of(-1.4426950408889634f, -1.4426950408889634f));
-  } else {
-    constexpr float k0 = -2.0f * 0.79788456080286536f * 1.4426950408889634f;
-    constexpr float k1 = 0.044715f * k0;
-    z = pair_mul(a, pair_fma(pair_mul(a, a), pair_of(k1, k1), pair_of(k0, k0)));
-  }
+// act() in fp32: a / (1 + 2^z) with z = -a log2(e) for SiLU, and for the tanh
+// form of GELU, a (1 + tanh u) / 2 = a / (1 + exp(-2 u)), z = -2 u log2(e), u =
+// sqrt(2 / pi) (a + 0.044715 a^3).  The exponential and the reciprocal are the
+// hardware's (relative error about 2^-21), far below the bf16 rounding of y.
+//
+// N pairs at a time, with one branch on the kind for all of them: a branch a
+// pair kept their chains of dependent instructions from running side by side.
+__device__ __forceinline__ uint64_t over_one_plus_exp2(uint64_t a, uint64_t z) {
   const float2 e = unpair(z);
   const float2 d = unpair(pair_add(pair_of(ex2_approx(e.x), ex2_approx(e.y)), pair_of(1.f, 1.f)));
   return pair_mul(a, pair_of(rcp_approx(d.x), rcp_approx(d.y)));
+}
+template <int N>
+__device__ __forceinline__ void activate(uint64_t (&v)[N], int act) {
+  if (act == CC3D_ACT_NONE) return;
+  if (act == CC3D_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      v[i] = over_one_plus_exp2(
+          v[i], pair_mul(v[i], pair_of(-1.4426950408889634f, -1.4426950408889634f)));
+  } else if (act == CC3D_ACT_GELU_TANH) {
+    constexpr float k0 = -2.0f * 0.79788456080286536f * 1.4426950408889634f;
+    constexpr float k1 = 0.044715f * k0;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      v[i] = over_one_plus_exp2(
+          v[i],
+          pair_mul(v[i], pair_fma(pair_mul(v[i], v[i]), pair_of(k1, k1), pair_of(k0, k0))));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float2 f = unpair(v[i]);
+      v[i] = pair_of(0.5f * f.x * erfcf(f.x * -0.70710678118654752f),
+                     0.5f * f.y * erfcf(f.y * -0.70710678118654752f));
+    }
+  }
 }
 
 // Columns of y that an epilogue warp finishes at a time: rows of 64 bytes in
@@ -372,39 +385,43 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float *bias = s_bias + u * kOutCols, *scale = s_scale + u * kOutCols;
-        float acc[32];
+        uint64_t v[kOutCols / 2];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) acc[e] = __uint_as_float(raw[e]);
+        for (int e = 0; e < kOutCols / 2; ++e)
+          v[e] = pair_of(__uint_as_float(raw[2 * e]), __uint_as_float(raw[2 * e + 1]));
         if ((u + 1) * kOutCols < cols) tmem_ld32_nowait(taddr + (u + 1) * kOutCols, raw);
         const uint64_t xs2 = pair_of(xs, xs);
 #pragma unroll
-        for (int g = 0; g < kOutCols; g += 8) {
-          uint4 *at = piece(ob, g / 8);
-          uint32_t rw[4] = {0u, 0u, 0u, 0u}, o[4];
-          if (p.residual) {
-            const uint4 r4 = *at;
-            rw[0] = r4.x;
-            rw[1] = r4.y;
-            rw[2] = r4.z;
-            rw[3] = r4.w;
+        for (int e = 0; e < kOutCols / 2; ++e) {
+          const uint64_t b2 = *reinterpret_cast<const uint64_t *>(bias + 2 * e);
+          if constexpr (FP8)
+            v[e] = pair_fma(v[e],
+                            pair_mul(xs2, *reinterpret_cast<const uint64_t *>(scale + 2 * e)), b2);
+          else
+            v[e] = pair_add(v[e], b2);
+        }
+        activate(v, p.act);
+        if (p.residual) {
+#pragma unroll
+          for (int g = 0; g < kOutCols / 8; ++g) {
+            const uint4 r4 = *piece(ob, g);
+            const uint32_t rw[4] = {r4.x, r4.y, r4.z, r4.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              v[4 * g + e] = pair_add(v[4 * g + e],
+                                      pair_of(__uint_as_float(rw[e] << 16),
+                                              __uint_as_float(rw[e] & 0xffff0000u)));
           }
+        }
+#pragma unroll
+        for (int g = 0; g < kOutCols / 8; ++g) {
+          uint32_t o[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int i = g + 2 * e;
-            const uint64_t b2 = *reinterpret_cast<const uint64_t *>(bias + i);
-            uint64_t v = pair_of(acc[i], acc[i + 1]);
-            if constexpr (FP8)
-              v = pair_fma(v, pair_mul(xs2, *reinterpret_cast<const uint64_t *>(scale + i)), b2);
-            else
-              v = pair_add(v, b2);
-            v = activate(v, p.act);
-            if (p.residual)
-              v = pair_add(v, pair_of(__uint_as_float(rw[e] << 16),
-                                      __uint_as_float(rw[e] & 0xffff0000u)));
-            const float2 f = unpair(v);
+            const float2 f = unpair(v[4 * g + e]);
             o[e] = pack_bf16x2(f.x, f.y);
           }
-          *at = make_uint4(o[0], o[1], o[2], o[3]);
+          *piece(ob, g) = make_uint4(o[0], o[1], o[2], o[3]);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -607,7 +624,9 @@ __global__ void __launch_bounds__(kSplitThreads)
       v[0] += b0;
       v[1] += b1;
       {
-        const float2 f = unpair(activate(pair_of(v[0], v[1]), p.act));
+        uint64_t a[1] = {pair_of(v[0], v[1])};
+        activate(a, p.act);
+        const float2 f = unpair(a[0]);
         v[0] = f.x;
         v[1] = f.y;
       }
