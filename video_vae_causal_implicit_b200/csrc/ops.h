@@ -55,22 +55,6 @@ struct AddNormArgs {
 // see what an earlier, overlapped kernel of the stream wrote)
 cudaError_t launch_add_rms_norm(const AddNormArgs &a, int sm_count, cudaStream_t stream);
 
-struct LinearArgs {
-  const float *x_scales, *w_scales;  // FP8: [m] (nullable) and [n]
-  const float *bias;                 // [n], nullable
-  const __nv_bfloat16 *residual;     // [m][ldr], nullable
-  __nv_bfloat16 *y;                  // [m][ldy]
-  long long ldy, ldr;
-  float x_scale;                     // FP8: where x_scales is null
-  int m, n, k, act;
-  int *status;
-  unsigned long long wait_limit_ns;
-  int nt, stages, split;             // set by launch_linear
-};
-// x [m][ldx] and w [n][ldw]: bf16, or E4M3 bytes (fp8).
-cudaError_t launch_linear(LinearArgs a, const void *x, long long ldx, const void *w,
-                          long long ldw, bool fp8, int sm_count, cudaStream_t stream);
-
 // x / d for 0 <= x < 2^31 by a multiplication (Granlund and Montgomery,
 // "Division by invariant integers using multiplication"): with l = ceil(log2
 // d) and mul = floor(2^32 (2^l - d) / d) + 1 the quotient is (x + (x mul >> 32)) >> l.
@@ -88,6 +72,24 @@ struct FastDiv {
   }
 #endif
 };
+
+struct LinearArgs {
+  const float *x_scales, *w_scales;  // FP8: [m] (nullable) and [n]
+  const float *bias;                 // [n], nullable
+  const __nv_bfloat16 *residual;     // [m][ldr], nullable
+  __nv_bfloat16 *y;                  // [m][ldy]
+  long long ldy, ldr;
+  float x_scale;                     // FP8: where x_scales is null
+  int m, n, k, act;
+  int *status;
+  unsigned long long wait_limit_ns;
+  // set by launch_linear: the tile and ring, and the walk over the tiles
+  int nt, stages, split, m_tiles, n_tiles;
+  FastDiv by_band, by_last;
+};
+// x [m][ldx] and w [n][ldw]: bf16, or E4M3 bytes (fp8).
+cudaError_t launch_linear(LinearArgs a, const void *x, long long ldx, const void *w,
+                          long long ldw, bool fp8, int sm_count, cudaStream_t stream);
 
 // Which frame of a sequence a cache slot holds: slot s < sinks frame s; the
 // later slots frame s (ring 0), or cyclically the last `ring` frames.
