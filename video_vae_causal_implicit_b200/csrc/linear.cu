@@ -56,10 +56,22 @@ __device__ __forceinline__ float rcp_approx(float x) {
 //
 // N pairs at a time, with one branch on the kind for all of them: a branch a
 // pair kept their chains of dependent instructions from running side by side.
+//
+// One reciprocal serves both of a pair, 1 / d0 = d1 / (d0 d1): the unit of the
+// exponential and the reciprocal (8 cycles a warp) bounds this part.  z up to
+// 62 keeps the product finite; beyond it |y| < 2^-56 |a| either way.
 __device__ __forceinline__ uint64_t over_one_plus_exp2(uint64_t a, uint64_t z) {
   const float2 e = unpair(z);
-  const float2 d = unpair(pair_add(pair_of(ex2_approx(e.x), ex2_approx(e.y)), pair_of(1.f, 1.f)));
-  return pair_mul(a, pair_of(rcp_approx(d.x), rcp_approx(d.y)));
+  const float2 d = unpair(pair_add(
+      pair_of(ex2_approx(fminf(e.x, 62.f)), ex2_approx(fminf(e.y, 62.f))), pair_of(1.f, 1.f)));
+  const float r = rcp_approx(d.x * d.y);
+  return pair_mul(a, pair_mul(pair_of(r, r), pair_of(d.y, d.x)));
+}
+// (a call: written out N times, its registers spill the other kinds' too)
+__device__ __noinline__ uint64_t gelu(uint64_t a) {
+  const float2 f = unpair(a);
+  return pair_of(0.5f * f.x * erfcf(f.x * -0.70710678118654752f),
+                 0.5f * f.y * erfcf(f.y * -0.70710678118654752f));
 }
 template <int N>
 __device__ __forceinline__ void activate(uint64_t (&v)[N], int act) {
@@ -79,11 +91,7 @@ __device__ __forceinline__ void activate(uint64_t (&v)[N], int act) {
           pair_mul(v[i], pair_fma(pair_mul(v[i], v[i]), pair_of(k1, k1), pair_of(k0, k0))));
   } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float2 f = unpair(v[i]);
-      v[i] = pair_of(0.5f * f.x * erfcf(f.x * -0.70710678118654752f),
-                     0.5f * f.y * erfcf(f.y * -0.70710678118654752f));
-    }
+    for (int i = 0; i < N; ++i) v[i] = gelu(v[i]);
   }
 }
 
@@ -387,7 +395,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < kOutCols / 2; ++e)
           v[e] = pair_of(__uint_as_float(raw[2 * e]), __uint_as_float(raw[2 * e + 1]));
-        if ((u + 1) * kOutCols < cols) tmem_ld32_nowait(taddr + (u + 1) * kOutCols, raw);
         const uint64_t xs2 = pair_of(xs, xs);
 #pragma unroll
         for (int e = 0; e < kOutCols / 2; e += 2) {
@@ -402,6 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         activate(v, p.act);
+        if ((u + 1) * kOutCols < cols) tmem_ld32_nowait(taddr + (u + 1) * kOutCols, raw);
         if (p.residual) {
 #pragma unroll
           for (int g = 0; g < kOutCols / 8; ++g) {
