@@ -180,3 +180,37 @@ def test_no_rows():
     before = cc3d.cc3d_launch_count()
     cc3d.linear(x[:0], w, y[:0])
     assert cc3d.cc3d_launch_count() == before and (y == 1).all()
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("m", [3, 700])
+def test_activation_over_its_whole_range(m, act):
+    """The bias alone through the activation: small and large values of both
+    signs, infinities (their limits: -inf gives 0, also where the formula in
+    floating point has no value) and NaN, whose neighbours keep theirs."""
+    n, k = 4096, 64
+    x = torch.zeros(m, k, device="cuda", dtype=torch.bfloat16)
+    w = torch.zeros(n, k, device="cuda", dtype=torch.bfloat16)
+    size = torch.logspace(-30, 30, n // 4, dtype=torch.float64)
+    near = torch.linspace(0, 150, n // 4, dtype=torch.float64)
+    bias = torch.stack([size, -size, near, -near], 1).flatten().float()
+    inf = float("inf")
+    odd = {0: inf, 3: -inf, 6: inf, 7: inf, 10: -inf, 11: -inf, 12: float("nan"),
+           17: float("nan"), 20: inf, 21: float("nan"), 24: -inf, 25: float("nan")}
+    for i, v in odd.items():
+        bias[i] = v
+    plain = torch.tensor([i not in odd for i in range(n)], device="cuda")
+    bias = bias.cuda()
+    y = torch.empty(m, n, device="cuda", dtype=torch.bfloat16)
+    cc3d.linear(x, w, y, bias=bias, act=act)
+    cc3d.sync_status()
+    ref, tol = reference(x, w, bias, None, act)
+    check(y[:, plain], ref[:, plain], tol[:, plain], "finite")
+    for i, v in odd.items():
+        got = y[:, i].float()
+        if v != v:
+            assert torch.isnan(got).all(), i
+        elif v == inf or act == cc3d.ACT_NONE:
+            assert (got == v).all(), i
+        else:
+            assert (got.abs() <= 2.0 ** -55).all(), i

@@ -49,29 +49,57 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// act() in fp32: a / (1 + 2^z) with z = -a log2(e) for SiLU, and for the tanh
-// form of GELU, a (1 + tanh u) / 2 = a / (1 + exp(-2 u)), z = -2 u log2(e), u =
-// sqrt(2 / pi) (a + 0.044715 a^3).  The exponential and the reciprocal are the
-// hardware's (relative error about 2^-21), far below the bf16 rounding of y.
+// act() in fp32, N pairs at a time.  One branch on the kind for all of them: a
+// branch a pair kept their chains of dependent instructions from running side
+// by side.
 //
-// N pairs at a time, with one branch on the kind for all of them: a branch a
-// pair kept their chains of dependent instructions from running side by side.
+// What bounds this part is the unit of the exponential and the reciprocal (8
+// cycles a warp each, relative error about 2^-21), so one reciprocal serves
+// both of a pair: 1 / d0 = d1 / (d0 d1).
 //
-// One reciprocal serves both of a pair, 1 / d0 = d1 / (d0 d1): the unit of the
-// exponential and the reciprocal (8 cycles a warp) bounds this part.  z up to
-// 62 keeps the product finite; beyond it |y| < 2^-56 |a| either way.
+//  * SiLU: a / (1 + 2^z), z = -a log2(e).
+//  * GELU, tanh form: a (1 + tanh u) / 2 = a / (1 + exp(-2 u)), z = -2 u
+//    log2(e), u = sqrt(2 / pi) (a + 0.044715 a^3).
+//    z up to 62 keeps the product of a pair finite; |y| < 2^-55 |a| beyond it.
+//    From below a counts as -128, so that -inf gives its limit, 0.
+//  * GELU, erf form: max(a, 0) - |a| h, h = erfc(x) / 2, x = |a| / sqrt(2), as
+//    h = t P(t) exp(-x^2) with t = 1 / (1 + x / 2).  P, of degree 8, is fitted
+//    to erfcx(x) / 2t for t in (0, 1]: relative error 6e-7 in fp32.  |a| counts
+//    as 64 at most (h is 0 there, and +-inf give their limits).
+// NaN stays NaN and leaves the pair's other value alone.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+// a / (1 + 2^z)
 __device__ __forceinline__ uint64_t over_one_plus_exp2(uint64_t a, uint64_t z) {
-  const float2 e = unpair(z);
+  const float2 e = unpair(z), f = unpair(a);
   const float2 d = unpair(pair_add(
       pair_of(ex2_approx(fminf(e.x, 62.f)), ex2_approx(fminf(e.y, 62.f))), pair_of(1.f, 1.f)));
   const float r = rcp_approx(d.x * d.y);
-  return pair_mul(a, pair_mul(pair_of(r, r), pair_of(d.y, d.x)));
+  return pair_mul(pair_of(max_nan(f.x, -128.f), max_nan(f.y, -128.f)),
+                  pair_mul(pair_of(r, r), pair_of(d.y, d.x)));
 }
-// (a call: written out N times, its registers spill the other kinds' too)
-__device__ __noinline__ uint64_t gelu(uint64_t a) {
+__device__ __forceinline__ uint64_t same(float x) { return pair_of(x, x); }
+__device__ __forceinline__ uint64_t gelu_erf(uint64_t a) {
   const float2 f = unpair(a);
-  return pair_of(0.5f * f.x * erfcf(f.x * -0.70710678118654752f),
-                 0.5f * f.y * erfcf(f.y * -0.70710678118654752f));
+  const uint64_t x = pair_of(fminf(fabsf(f.x), 64.f), fminf(fabsf(f.y), 64.f));  // |a|
+  const float2 d = unpair(pair_fma(x, same(0.35355339f), same(1.f)));
+  const float2 z = unpair(pair_mul(pair_mul(x, x), same(-0.72134752f)));
+  const float r = rcp_approx(d.x * d.y);
+  const uint64_t t = pair_mul(same(r), pair_of(d.y, d.x));
+  uint64_t h = same(-0.021936405f);
+  h = pair_fma(h, t, same(0.11050928f));
+  h = pair_fma(h, t, same(-0.18864024f));
+  h = pair_fma(h, t, same(0.08819317f));
+  h = pair_fma(h, t, same(0.013868884f));
+  h = pair_fma(h, t, same(0.09287188f));
+  h = pair_fma(h, t, same(0.12302662f));
+  h = pair_fma(h, t, same(0.14105959f));
+  h = pair_fma(h, t, same(0.14104733f));
+  h = pair_mul(pair_mul(h, t), pair_of(ex2_approx(z.x), ex2_approx(z.y)));
+  return pair_fma(pair_mul(x, same(-1.f)), h, pair_of(max_nan(f.x, 0.f), max_nan(f.y, 0.f)));
 }
 template <int N>
 __device__ __forceinline__ void activate(uint64_t (&v)[N], int act) {
@@ -79,19 +107,17 @@ __device__ __forceinline__ void activate(uint64_t (&v)[N], int act) {
   if (act == CC3D_ACT_SILU) {
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      v[i] = over_one_plus_exp2(
-          v[i], pair_mul(v[i], pair_of(-1.4426950408889634f, -1.4426950408889634f)));
+      v[i] = over_one_plus_exp2(v[i], pair_mul(v[i], same(-1.4426950408889634f)));
   } else if (act == CC3D_ACT_GELU_TANH) {
     constexpr float k0 = -2.0f * 0.79788456080286536f * 1.4426950408889634f;
     constexpr float k1 = 0.044715f * k0;
 #pragma unroll
     for (int i = 0; i < N; ++i)
       v[i] = over_one_plus_exp2(
-          v[i],
-          pair_mul(v[i], pair_fma(pair_mul(v[i], v[i]), pair_of(k1, k1), pair_of(k0, k0))));
+          v[i], pair_mul(v[i], pair_fma(pair_mul(v[i], v[i]), same(k1), same(k0))));
   } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = gelu(v[i]);
+    for (int i = 0; i < N; ++i) v[i] = gelu_erf(v[i]);
   }
 }
 
