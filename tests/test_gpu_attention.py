@@ -270,6 +270,56 @@ def test_infinite_key_and_nan_value_are_as_in_the_definition():
     assert torch.isnan(o[0, 0, 0, 5]) and torch.isfinite(o[0, 0, 0, :5].float()).all()
 
 
+HIDDEN = {
+    "tokens": dict(t=200, total=200, d=64, heads=4, kv=2, window=50),
+    "tokens sinks": dict(t=300, total=700, d=128, heads=2, kv=1, window=100, sinks=2),
+    "no window": dict(t=70, total=70, d=40, heads=1, kv=1),
+    "many rows": dict(t=2000, total=2000, d=128, heads=8, kv=8, window=300),
+    "shared heads": dict(t=500, total=900, d=64, heads=32, kv=4, window=0),
+    "split keys": dict(t=4, total=3001, d=128, heads=8, kv=2, window=0),
+    "wide frames": dict(frame=10, t=20, total=30, d=384, window=3),
+    "wide": dict(frame=7, t=9, total=40, d=200, window=5, sinks=1, heads=2, kv=2),
+    "ring": dict(frame=16, t=6, total=40, d=64, heads=2, kv=2, window=6, sinks=1, ring=12),
+    "lengths": dict(n=3, t=40, d=128, heads=4, kv=2, window=30, k_frames=[60, 40, 130],
+                    q_frames=[40, 17, 33]),
+}
+
+
+@pytest.mark.parametrize("name", list(HIDDEN))
+def test_values_that_are_not_finite_reach_the_queries_that_see_them_alone(name):
+    """Infinities and NaN in values that some queries of the chunk see and
+    others, in the same tile of rows, do not."""
+    c = Case(**HIDDEN[name], seed=8)
+    kinds = [float("inf"), float("nan"), -float("inf")]
+    put = []  # sequence, key, kv head, channel, value; a channel is used once
+    for b in range(c.n):
+        keys = c.all[b] * c.f
+        first = max(0, (c.all[b] - c.chunk[b]) * c.f)
+        at = sorted({0, 1, first, first + 1, first + 3, (first + keys) // 2, keys - 2, keys - 1,
+                     max(0, first - 7), keys // 2})
+        for i, key in enumerate(x for x in at if 0 <= x < keys):
+            put.append((b, key, i % c.kv, (5 * i + 3) % c.d, kinds[i % 3]))
+    for b, key, h, ch, value in put:
+        c.lv[b, key, h, ch] = value
+    o = c.run()
+    for b, key, h, ch, _ in put:
+        c.lv[b, key, h, ch] = 0
+    group = c.heads // c.kv
+    for b in range(c.n):
+        rows = c.chunk[b] * c.f
+        ref, tol = c.reference(b)
+        got = o[b, :rows].double()
+        good = (got - ref).abs() <= tol
+        seen = c.seen(b)
+        for _, key, h, ch, value in [x for x in put if x[0] == b]:
+            for head in range(h * group, (h + 1) * group):
+                mine = got[:, head, ch][seen[:, key]]
+                assert (torch.isnan(mine) if value != value else mine == value).all(), (key, ch)
+                good[:, head, ch] |= seen[:, key]
+        assert good.all(), (b, int((~good).sum()), (~good).nonzero()[:3].tolist())
+        assert (o[b, rows:] == 7).all()
+
+
 @pytest.mark.parametrize("name", ["token", "prefill window", "ring chunk", "frame large",
                                   "ring frames many"])
 def test_same_bytes_on_every_call_stream_and_replay(name):
@@ -372,8 +422,8 @@ def test_streaming_token_by_token_equals_the_whole_sequence():
 
 
 def test_long_cache_offsets_past_32_bits():
-    """A cache of more than 2^31 elements: 20 sequences, 1 million tokens each,
-    of which the last is read."""
+    """A cache of more than 2^31 elements: 9 sequences of a million tokens, of
+    which the last ones and the sinks are read."""
     n, slots, kv, d = 9, 1 << 20, 2, 128
     assert n * slots * kv * d > 1 << 31
     k = torch.zeros(n, slots, kv, d, device="cuda", dtype=torch.bfloat16)

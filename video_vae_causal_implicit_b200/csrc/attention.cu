@@ -169,7 +169,7 @@ struct Shape {
   // Shared memory: Q, the ring of groups (after them, in a split, the parts
   // of the rows in their place), barriers, the rows' (maximum, sum).
   static constexpr uint32_t rest(int stages) {
-    return 8u * (2u * stages + 4u + 6u * NQ) + 16u + NQ * kRows * 8u + 1024u;
+    return 8u * (2u * stages + 6u + 6u * NQ) + 32u + NQ * kRows * 8u + 1024u;
   }
   static constexpr int stages() {
     int st = 24;
@@ -317,6 +317,67 @@ __device__ __forceinline__ void finish_rows(const AttnArgs &p, int rank, int row
   }
 }
 
+// A bit per key of a tile.
+template <int W>
+struct Bits {
+  uint32_t w[W];
+  __device__ __forceinline__ bool any() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) m |= w[i];
+    return m != 0;
+  }
+};
+
+// O[row] += P[row][s] V[s] for the keys s that are taken apart, in the rows
+// that see them.  v: the tile's first value in the cache; the columns of this
+// warp's rows: o of O, sc of P (two weights a column).
+template <int W>
+__device__ __noinline__ void add_apart(const __nv_bfloat16 *v, long long v_tok, int d, uint32_t sc,
+                                       uint32_t o, int o_cols, Bits<W> keys, Bits<W> seen,
+                                       bool begin) {
+#pragma unroll 1
+  for (int i = 0; i < o_cols; i += 32) {
+    uint32_t acc[32];
+#pragma unroll
+    for (int e = 0; e < 32; ++e) acc[e] = 0u;
+    if (!begin) {
+      tmem_ld32_nowait(o + i, acc);
+      tmem_wait_ld();
+      tmem_regs_after_wait<32>(acc);
+    }
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+#pragma unroll 1
+      for (uint32_t left = keys.w[w]; left; left &= left - 1) {  // (the same in every lane)
+        const int s = __ffs(left) - 1;
+        uint32_t two[1] = {tmem_ld1_nowait(sc + (32 * w + s) / 2)};
+        tmem_wait_ld();
+        tmem_regs_after_wait<1>(two);
+        const float weight = __uint_as_float(s & 1 ? two[0] & 0xffff0000u : two[0] << 16);
+        const __nv_bfloat16 *at = v + (32 * w + s) * v_tok + i;
+        if (seen.w[w] >> s & 1u) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+            if (i + e < d) {
+              const uint4 x = *reinterpret_cast<const uint4 *>(at + e);
+              const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                float *a = reinterpret_cast<float *>(&acc[e + 2 * k]);
+                a[0] = fmaf(weight, __uint_as_float(u[k] << 16), a[0]);
+                a[1] = fmaf(weight, __uint_as_float(u[k] & 0xffff0000u), a[1]);
+              }
+            }
+        }
+        __syncwarp();
+      }
+    }
+    tmem_st32(o + i, acc);
+  }
+  tmem_wait_st();
+}
+
 // NQ row tiles of 128, key tiles of KT tokens.  Every row tile has two slots
 // for its scores, so that the scores of the next key tile are there when the
 // softmax of one ends.
@@ -347,8 +408,12 @@ __global__ void __launch_bounds__(attn_threads(NQ), OCC)
   uint64_t *pv_done = p_ready + 2 * NQ;   // [NQ][2]
   uint64_t *o_full = pv_done + 2 * NQ;
   uint64_t *drain = o_full + 1;           // [2]
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 2);
-  float2 *row_ml = reinterpret_cast<float2 *>(tmem_slot + 2);  // [NQ * 128] (split)
+  uint64_t *v_clean = drain + 2;
+  uint64_t *v_taken = v_clean + 1;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(v_taken + 1);
+  uint32_t *apart = tmem_slot + 2;                              // [4] keys of a tile
+  volatile int *o_begun = reinterpret_cast<int *>(apart + 4);   // [2]
+  float2 *row_ml = reinterpret_cast<float2 *>(tmem_slot + 8);   // [NQ * 128] (split)
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -356,7 +421,7 @@ __global__ void __launch_bounds__(attn_threads(NQ), OCC)
   if (threadIdx.x == 0) {
     for (int i = 0; i < stages; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], NQ);  // (each row tile's products)
+      mbar_init(&empty[i], NQ + 1);  // (each row tile's products, and warp 3)
     }
     mbar_init(q_full, 1);
     for (int i = 0; i < 2 * NQ; ++i) {
@@ -367,6 +432,9 @@ __global__ void __launch_bounds__(attn_threads(NQ), OCC)
     mbar_init(o_full, NQ);
     mbar_init(&drain[0], 1);
     mbar_init(&drain[1], 1);
+    mbar_init(v_clean, 1);
+    mbar_init(v_taken, 4 * NQ);
+    o_begun[0] = o_begun[1] = 0;
     fence_mbar_init();
     prefetch_tmap(&map_q);
     prefetch_tmap(&map_k);
@@ -554,7 +622,7 @@ __global__ void __launch_bounds__(attn_threads(NQ), OCC)
         for (int j = 0; j < nj && ok; ++j) {
           if (!await(&p_ready[2 * q + (j & 1)], (j >> 1) & 1, 33)) break;
           tc_fence_after();
-          values(q, j & 1, v, j == 0);
+          values(q, j & 1, v, j == 0 && !o_begun[q]);
           advance(v, j + 2 < nj ? 2 : 1);
           if (j + 2 < nj && ok) {
             scores(q, j & 1, k);
@@ -575,7 +643,7 @@ __global__ void __launch_bounds__(attn_threads(NQ), OCC)
         for (int j = 0; j < nj && ok; ++j) {
           if (!await(&p_ready[j & 1], (j >> 1) & 1, 33)) break;
           tc_fence_after();
-          values(0, j & 1, v, j == 0);
+          values(0, j & 1, v, j == 0 && !o_begun[0]);
           advance(v, j + 2 < nj ? 2 : 1);
         }
       }
@@ -620,7 +688,7 @@ __global__ void __launch_bounds__(attn_threads(NQ), OCC)
         if (wg == 0 || j + 1 < nj) named_barrier_arrive(2 - wg, 256);
     };
     if (NQ == 2 && wg == 1 && nj > 0) named_barrier_arrive(1, 256);
-    int tile = nj > 0 ? tiles.at(j0) : 0;
+    int tile = nj > 0 ? tiles.at(j0) : 0, n_masked = 0;
 #pragma unroll 1
     for (int j = 0; j < nj; ++j, tile = tiles.after(tile, j0 + j)) {
       const int t0 = tile * KT;
@@ -701,27 +769,27 @@ __global__ void __launch_bounds__(attn_threads(NQ), OCC)
       }
       pass_turn(j);
       tmem_wait_st();
-      if (masked && !any.covers(t0, t0 + KT)) {
-        // Values no query of the CTA sees may be anything (a slot never
-        // written, a frame beyond the end): 0 times a NaN would reach the
-        // sums, so their rows are cleared before the products read them (by
-        // both row tiles, each before its own products).
-        const int pos = ((j + 1 < nj ? j + 2 : nj) + j) * NG;
-        for (int g = 0; g < NG; ++g) {
-          const int sl = (pos + g) % stages;
-          ok = await(&full[sl], static_cast<uint32_t>((pos + g) / stages) & 1u, 37);
-          if (!ok) break;
-          if (r < KT && !any.has(t0 + r)) {
-            uint4 *row =
-                reinterpret_cast<uint4 *>(smem + S::kQ + sl * S::kGroup + r * 128);
-            for (int c = 0; c < GC; ++c)
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                row[c * (S::kChunk / 16) + e] = make_uint4(0, 0, 0, 0);
-          }
-        }
+      if (masked) {
+        ok = await(v_clean, static_cast<uint32_t>(n_masked++) & 1u, 37);
         if (!ok) continue;
-        fence_proxy_async_smem();
+        Bits<KT / 32> keys;
+#pragma unroll
+        for (int i = 0; i < KT / 32; ++i) keys.w[i] = apart[i];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v_taken);
+        if (keys.any()) {
+          if (j > 0) {
+            ok = await(&pv_done[2 * wg + (slot ^ 1)], static_cast<uint32_t>((j - 1) >> 1) & 1u, 40);
+            if (!ok) continue;
+            tc_fence_after();
+          }
+          Bits<KT / 32> seen;
+#pragma unroll
+          for (int i = 0; i < KT / 32; ++i) seen.w[i] = mine.bits(t0 + 32 * i);
+          add_apart(p.v + seq * p.v_seq + t0 * p.v_tok + kv_head * p.v_head, p.v_tok, cs.d, sc,
+                    o_col + wg * o_cols + lanes, static_cast<int>(o_cols), keys, seen, j == 0);
+          if (j == 0 && lane == 0) o_begun[wg] = 1;
+        }
       }
       tc_fence_before();
       __syncwarp();
@@ -780,7 +848,109 @@ __global__ void __launch_bounds__(attn_threads(NQ), OCC)
     }
     if (split > 1) row_ml[wg * kRows + r] = make_float2(m, l);
   } else {
+    // ------------------------------ values behind a mask --------------------------
+    // A weight of 0 times an infinity or a NaN would reach the sums, so in the
+    // tiles that a mask cuts, values no query of the CTA sees are cleared
+    // before the products read them (they may be anything: a slot never
+    // written, a frame beyond the end), and so are keys' values that are not
+    // finite where only some queries see them: the rows that do add those
+    // apart.  (The warp passes every group of the ring, so that no barrier
+    // runs ahead of it.)
     if constexpr (NQ == 2) regs_fewer<kRegsFew>();
+    griddep_wait();
+    constexpr int kMine = KT / 32;  // keys of a lane: lane, lane + 32, ...
+    int s = 0;
+    uint32_t ph = 0, n_masked = 0;
+    auto landed = [&](int n) {  // the ring's next n groups
+      int at = s;
+      uint32_t par = ph;
+      for (int g = 0; g < n && ok; ++g) {
+        ok = __all_sync(0xffffffffu, mbar_wait_soon(&full[at], par, p.wait_limit_ns, p.status,
+                                                    42)) != 0;
+        if (++at == stages) { at = 0; par ^= 1; }
+      }
+      return ok;
+    };
+    auto pass = [&](int n) {
+      __syncwarp();
+      for (int g = 0; g < n; ++g) {
+        if (lane == 0) mbar_arrive(&empty[s]);
+        if (++s == stages) { s = 0; ph ^= 1; }
+      }
+    };
+    int tile = nj > 0 ? tiles.at(j0) : 0;
+    if (nj > 0 && landed(NG)) pass(NG);  // K 0, K 1, V 0, K 2, V 1, ...
+#pragma unroll 1
+    for (int j = 0; j < nj && ok; ++j, tile = tiles.after(tile, j0 + j)) {
+      if (j + 1 < nj) {
+        if (!landed(NG)) break;
+        pass(NG);
+      }
+      if (!landed(NG)) break;
+      const int t0 = tile * KT;
+      if (every.covers(t0, t0 + KT)) {
+        pass(NG);
+        continue;
+      }
+      uint32_t hidden = 0, some = 0;  // bit i: key lane + 32 i
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int t = t0 + 32 * i + lane;
+        if (!any.has(t)) hidden |= 1u << i;
+        else if (!every.has(t)) some |= 1u << i;
+      }
+      auto group = [&](int g) {
+        const int at = s + g < stages ? s + g : s + g - stages;
+        return smem + S::kQ + at * S::kGroup + lane * 128;
+      };
+      uint32_t odd = 0;  // keys that some see with a value that is not finite
+      if (some) {
+#pragma unroll 1
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+          for (int i = 0; i < kMine; ++i) {
+            if (!(some >> i & 1u)) continue;
+            uint32_t top = 0;  // (exponents of ones carry into bits 15 and 31)
+#pragma unroll
+            for (int c = 0; c < GC; ++c)
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {  // (in an order that meets every bank once)
+                const uint4 x = *reinterpret_cast<const uint4 *>(
+                    group(g) + c * S::kChunk + i * 4096 + (((e + lane) & 7) << 4));
+                top |= (x.x & 0x7f807f80u) + 0x00800080u;
+                top |= (x.y & 0x7f807f80u) + 0x00800080u;
+                top |= (x.z & 0x7f807f80u) + 0x00800080u;
+                top |= (x.w & 0x7f807f80u) + 0x00800080u;
+              }
+            if (top & 0x80008000u) odd |= 1u << i;
+          }
+      }
+      const uint32_t clear = hidden | odd;
+      if (clear)
+        for (int g = 0; g < NG; ++g)
+          for (int i = 0; i < kMine; ++i)
+            if (clear >> i & 1u)
+              for (int c = 0; c < GC; ++c)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  *reinterpret_cast<uint4 *>(group(g) + c * S::kChunk + i * 4096 +
+                                             (((e + lane) & 7) << 4)) = make_uint4(0, 0, 0, 0);
+      fence_proxy_async_smem();
+      // (the tile before's have been read)
+      if (n_masked > 0)
+        ok = __all_sync(0xffffffffu, mbar_wait_soon(v_taken, (n_masked - 1) & 1u, p.wait_limit_ns,
+                                                    p.status, 43)) != 0;
+      if (!ok) break;
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const uint32_t bits = __ballot_sync(0xffffffffu, odd >> i & 1u);
+        if (lane == 0) apart[i] = bits;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(v_clean);
+      ++n_masked;
+      pass(NG);
+    }
   }
   if (split > 1) {
     __syncwarp();

@@ -105,7 +105,8 @@ struct AttnArgs {
   int heads, window;       // window: frames, 0 = unlimited
   float scale_log2;        // softmax scale * log2(e)
   __nv_bfloat16 *o;
-  long long o_seq, o_tok, o_head;
+  const __nv_bfloat16 *v;  // (read apart from the tiles where a value is not finite)
+  long long o_seq, o_tok, o_head, v_seq, v_tok, v_head;
   int *status;
   unsigned long long wait_limit_ns;
   int group, tok_tile;     // query heads per kv head; tokens per 128 rows

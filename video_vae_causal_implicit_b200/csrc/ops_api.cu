@@ -294,6 +294,10 @@ cc3d_status cc3d_attention(const cc3d_attn_call *p, void *stream) {
   const float scale = p->scale > 0.f ? p->scale : 1.f / sqrtf(static_cast<float>(p->d));
   a.scale_log2 = scale * 1.4426950408889634f;
   a.o = static_cast<__nv_bfloat16 *>(p->o);
+  a.v = static_cast<const __nv_bfloat16 *>(p->v);
+  a.v_seq = p->v_seq;
+  a.v_tok = p->v_tok;
+  a.v_head = p->v_head;
   a.o_seq = p->o_seq;
   a.o_tok = p->o_tok;
   a.o_head = p->o_head;
