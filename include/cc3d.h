@@ -488,8 +488,8 @@ cc3d_status cc3d_linear(const cc3d_linear_call *call, void *stream);
  * `slots` frames per sequence.  ring == 0: slot s holds frame s.  ring > 0
  * (slots == sinks + ring): slots below `sinks` hold the first frames, frame
  * p >= sinks is in slot sinks + (p - sinks) % ring; the ring has to hold what
- * the chunk sees, window - 1 + t <= ring.  Slots that no query sees may hold
- * anything, NaN included.
+ * the chunk sees, window - 1 + t <= ring.  Keys and values that a query does
+ * not see do not reach it, whatever they hold, NaN included.
  *
  * q and o [n][t * frame][heads][d], k and v [n][slots * frame][kv_heads][d],
  * each with its own strides in elements (multiples of 8; the last dimension

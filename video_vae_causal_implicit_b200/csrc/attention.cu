@@ -25,7 +25,11 @@
 //
 // Bound: the tensor pipe and the exponentials (16 a cycle and SM, as many
 // cycles as the two products take at d = 128) for many rows, the cache's
-// bytes for one token.
+// bytes for one token.  Measured: 8190 tokens, 16 heads on 4 of d = 128, window
+// 2048 and 4 sinks 124 us (970 TFLOP/s; a step of 64 keys takes a CTA's 256
+// rows about 1700 cycles, of which the products want 1130 and the exponentials
+// 1024); frames of 1560 tokens, d = 384, within themselves 31 us for five; one
+// token of 8 sequences, 32 heads on 8, over 8208 cached 47 us (5.7 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -155,9 +159,10 @@ __device__ __forceinline__ void lengths(const CacheShape &c, int seq, int &chunk
 
 // Shapes of a kernel: NQ row tiles of 128, key tiles of KT tokens, CH chunks
 // of 64 channels.  Keys and values travel in groups of GC chunks, NG a tile,
-// one barrier each: whole tiles where several fit beside Q, single chunks for
+// one barrier each: whole tiles where several fit beside Q, pairs of chunks for
 // wide heads (a slot is then free, and its next load on its way, as soon as
-// four products have read it).  P V runs in steps of PC chunks (N = 64 PC).
+// the products of one pair have read it; at d = 384 threes measured 4 % slower
+// and single chunks 3 %).  P V runs in steps of PC chunks (N = 64 PC).
 template <int NQ, int KT, int CH, int OCC>
 struct Shape {
   static constexpr int GC = CH <= 2 ? CH : 2;
@@ -197,8 +202,8 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// Warps 0 - 3: loads, products (two), an idle one (the registers of a warpgroup
-// can be moved only together); then four warps per row tile.
+// Warps 0 - 3: loads, products (two), values behind a mask; then four warps per
+// row tile.
 constexpr int kFirstRowWarp = 4;
 constexpr __host__ __device__ int attn_threads(int nq) { return 32 * kFirstRowWarp + 128 * nq; }
 // 168 registers a thread at launch with 384 threads; the row warps' tile of
@@ -329,6 +334,53 @@ struct Bits {
   }
 };
 
+// Of the keys in `some` (bit i: key lane + 32 i of the value tile in the ring's
+// groups s, s + 1, ...) those with a value that is not finite; their values
+// are cleared.  (A call, as is the other part: written into the kernel they
+// cost one token's step over a long cache 3 to 5 of its 47 us.)
+template <int KT, int GC, int NG>
+__device__ __noinline__ uint32_t take_apart(uint8_t *ring, int s, int stages, uint32_t some) {
+  constexpr uint32_t kChunk = KT * 128u;
+  const int lane = threadIdx.x % 32;
+  auto group = [&](int g) {
+    return ring + (s + g < stages ? s + g : s + g - stages) * (GC * kChunk) + lane * 128;
+  };
+  uint32_t odd = 0;
+#pragma unroll 1
+  for (int g = 0; g < NG; ++g)
+#pragma unroll
+    for (int i = 0; i < KT / 32; ++i) {
+      if (!(some >> i & 1u)) continue;
+      uint32_t top = 0;  // (exponents of ones carry into bits 15 and 31)
+#pragma unroll
+      for (int c = 0; c < GC; ++c)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {  // (in an order that meets every bank once)
+          const uint4 x = *reinterpret_cast<const uint4 *>(group(g) + c * kChunk + i * 4096 +
+                                                           (((e + lane) & 7) << 4));
+          top |= (x.x & 0x7f807f80u) + 0x00800080u;
+          top |= (x.y & 0x7f807f80u) + 0x00800080u;
+          top |= (x.z & 0x7f807f80u) + 0x00800080u;
+          top |= (x.w & 0x7f807f80u) + 0x00800080u;
+        }
+      if (top & 0x80008000u) odd |= 1u << i;
+    }
+  if (odd) {
+#pragma unroll 1
+    for (int g = 0; g < NG; ++g)
+#pragma unroll 1
+      for (int i = 0; i < KT / 32; ++i)
+        if (odd >> i & 1u)
+          for (int c = 0; c < GC; ++c)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<uint4 *>(group(g) + c * kChunk + i * 4096 + e * 16) =
+                  make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+  }
+  return odd;
+}
+
 // O[row] += P[row][s] V[s] for the keys s that are taken apart, in the rows
 // that see them.  v: the tile's first value in the cache; the columns of this
 // warp's rows: o of O, sc of P (two weights a column).
@@ -385,9 +437,9 @@ __device__ __noinline__ void add_apart(const __nv_bfloat16 *v, long long v_tok, 
 // Measured alone, M = 128 products with both operands in shared memory (Q K^T)
 // take N / 2 + 44 cycles, with A in tensor memory (P V) N / 2 + 10, and
 // alternating N / 2 each: the first kind loads its A under the second's
-// product.  One thread cannot issue them that fast (a barrier wait costs it
-// some 130 cycles, a product 40), so two warps do: one per row tile, or one
-// per kind.
+// product.  One thread cannot issue them that fast (a product costs it some 40
+// cycles, a barrier's wait 40 to 130), so two warps do: one per row tile, or
+// one per kind.
 template <int NQ, int KT, int CH, int OCC>
 __global__ void __launch_bounds__(attn_threads(NQ), OCC)
     attn_kernel(const __grid_constant__ CUtensorMap map_q,
@@ -777,6 +829,19 @@ __global__ void __launch_bounds__(attn_threads(NQ), OCC)
         for (int i = 0; i < KT / 32; ++i) keys.w[i] = apart[i];
         __syncwarp();
         if (lane == 0) mbar_arrive(v_taken);
+        if (r < KT && !any.has(t0 + r)) {
+          // (K 0, K 1, V 0, K 2, V 1, ... in the ring)
+          int at = (((j + 1 < nj ? j + 2 : nj) + j) * NG) % stages;
+#pragma unroll 1
+          for (int g = 0; g < NG; ++g) {
+            uint4 *row = reinterpret_cast<uint4 *>(smem + S::kQ + at * S::kGroup + r * 128);
+            for (int u = 0; u < GC; ++u)
+#pragma unroll
+              for (int e = 0; e < 8; ++e) row[u * (S::kChunk / 16) + e] = make_uint4(0, 0, 0, 0);
+            if (++at == stages) at = 0;
+          }
+        }
+        fence_proxy_async_smem();
         if (keys.any()) {
           if (j > 0) {
             ok = await(&pv_done[2 * wg + (slot ^ 1)], static_cast<uint32_t>((j - 1) >> 1) & 1u, 40);
@@ -849,13 +914,13 @@ __global__ void __launch_bounds__(attn_threads(NQ), OCC)
     if (split > 1) row_ml[wg * kRows + r] = make_float2(m, l);
   } else {
     // ------------------------------ values behind a mask --------------------------
-    // A weight of 0 times an infinity or a NaN would reach the sums, so in the
-    // tiles that a mask cuts, values no query of the CTA sees are cleared
-    // before the products read them (they may be anything: a slot never
-    // written, a frame beyond the end), and so are keys' values that are not
-    // finite where only some queries see them: the rows that do add those
-    // apart.  (The warp passes every group of the ring, so that no barrier
-    // runs ahead of it.)
+    // A weight of 0 times an infinity or a NaN would reach the sums.  So in the
+    // tiles that a mask cuts, keys' values that are not finite where only some
+    // queries see them are cleared before the products read them, and the rows
+    // that do see them add them apart.  Values no query of the CTA sees (they
+    // may be anything: a slot never written, a frame beyond the end) are
+    // cleared by the row warps once this warp says that they have landed: it
+    // passes every group of the ring, so that no barrier runs ahead of it.
     if constexpr (NQ == 2) regs_fewer<kRegsFew>();
     griddep_wait();
     constexpr int kMine = KT / 32;  // keys of a lane: lane, lane + 32, ...
@@ -892,50 +957,15 @@ __global__ void __launch_bounds__(attn_threads(NQ), OCC)
         pass(NG);
         continue;
       }
-      uint32_t hidden = 0, some = 0;  // bit i: key lane + 32 i
+      uint32_t some = 0;  // bit i: key lane + 32 i
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
         const int t = t0 + 32 * i + lane;
-        if (!any.has(t)) hidden |= 1u << i;
-        else if (!every.has(t)) some |= 1u << i;
+        if (any.has(t) && !every.has(t)) some |= 1u << i;
       }
-      auto group = [&](int g) {
-        const int at = s + g < stages ? s + g : s + g - stages;
-        return smem + S::kQ + at * S::kGroup + lane * 128;
-      };
-      uint32_t odd = 0;  // keys that some see with a value that is not finite
-      if (some) {
-#pragma unroll 1
-        for (int g = 0; g < NG; ++g)
-#pragma unroll
-          for (int i = 0; i < kMine; ++i) {
-            if (!(some >> i & 1u)) continue;
-            uint32_t top = 0;  // (exponents of ones carry into bits 15 and 31)
-#pragma unroll
-            for (int c = 0; c < GC; ++c)
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {  // (in an order that meets every bank once)
-                const uint4 x = *reinterpret_cast<const uint4 *>(
-                    group(g) + c * S::kChunk + i * 4096 + (((e + lane) & 7) << 4));
-                top |= (x.x & 0x7f807f80u) + 0x00800080u;
-                top |= (x.y & 0x7f807f80u) + 0x00800080u;
-                top |= (x.z & 0x7f807f80u) + 0x00800080u;
-                top |= (x.w & 0x7f807f80u) + 0x00800080u;
-              }
-            if (top & 0x80008000u) odd |= 1u << i;
-          }
-      }
-      const uint32_t clear = hidden | odd;
-      if (clear)
-        for (int g = 0; g < NG; ++g)
-          for (int i = 0; i < kMine; ++i)
-            if (clear >> i & 1u)
-              for (int c = 0; c < GC; ++c)
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  *reinterpret_cast<uint4 *>(group(g) + c * S::kChunk + i * 4096 +
-                                             (((e + lane) & 7) << 4)) = make_uint4(0, 0, 0, 0);
-      fence_proxy_async_smem();
+      uint32_t odd = 0;
+      if (__any_sync(0xffffffffu, some))
+        odd = take_apart<KT, GC, NG>(smem + S::kQ, s, stages, some);
       // (the tile before's have been read)
       if (n_masked > 0)
         ok = __all_sync(0xffffffffu, mbar_wait_soon(v_taken, (n_masked - 1) & 1u, p.wait_limit_ns,
