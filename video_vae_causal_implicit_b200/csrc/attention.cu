@@ -161,8 +161,9 @@ __device__ __forceinline__ void lengths(const CacheShape &c, int seq, int &chunk
 // of 64 channels.  Keys and values travel in groups of GC chunks, NG a tile,
 // one barrier each: whole tiles where several fit beside Q, pairs of chunks for
 // wide heads (a slot is then free, and its next load on its way, as soon as
-// the products of one pair have read it; at d = 384 threes measured 4 % slower
-// and single chunks 3 %).  P V runs in steps of PC chunks (N = 64 PC).
+// the products of one pair have read it; single chunks, with twice the
+// barriers, took 38.5 us where pairs take 30.7: five frames of 1560 tokens, d =
+// 384).  P V runs in steps of PC chunks (N = 64 PC).
 template <int NQ, int KT, int CH, int OCC>
 struct Shape {
   static constexpr int GC = CH <= 2 ? CH : 2;
