@@ -148,3 +148,21 @@ def test_nan_stays_in_its_row():
     keep = torch.arange(9, device="cuda") != 4
     assert torch.equal(q.view(torch.uint8)[keep], q2.view(torch.uint8)[keep])
     assert torch.equal(s[keep], s2[keep]) and torch.isnan(q2[4].float()).any()
+
+
+@pytest.mark.parametrize("c", [64, 384, 1024, 2048, 8192])
+def test_nan_and_infinities_are_as_in_the_definition(c):
+    """A NaN makes its whole row NaN (its sum of squares is); an infinity makes
+    itself NaN and the rest of its row 0.  Codes of such rows: scale 1."""
+    x, _, gamma, _ = make(6, c, 9)
+    x[1, c // 2], x[3, 5], x[4, 0] = float("nan"), float("inf"), -float("inf")
+    y, q = torch.empty_like(x), torch.empty_like(x, dtype=torch.float8_e4m3fn)
+    s = torch.empty(6, device="cuda")
+    cc3d.add_rms_norm(x, gamma, y=y, q=q, scales=s)
+    cc3d.sync_status()
+    a, _ = reference(x, gamma, None, 0.0, False)
+    assert torch.equal(torch.isnan(y), torch.isnan(a)) and torch.isnan(y[1]).all()
+    assert torch.equal(torch.isnan(q.float()), torch.isnan(a))
+    rest = ~torch.isnan(a[[3, 4]])
+    assert (y[[3, 4]][rest] == 0).all() and (q.float()[[3, 4]][rest] == 0).all()
+    assert (s[[1, 3, 4]] == 1).all() and (s[[0, 2, 5]] < 1).all()

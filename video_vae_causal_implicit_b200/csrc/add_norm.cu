@@ -88,7 +88,10 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) add_norm_kernel(const A
 #pragma unroll
       for (int i = 0; i < kWarps; ++i) ss += red[0][i];
     }
-    const float inv = root_c / fmaxf(sqrtf(fmaf(fc, p.eps, ss)), 1e-12f);
+    // (not fmaxf, which would put 1e-12 in the place of a NaN and leave the
+    // row's other elements finite)
+    const float norm = sqrtf(fmaf(fc, p.eps, ss));
+    const float inv = root_c / (norm < 1e-12f ? 1e-12f : norm);
     float a[CPT][8];
     float top = 0.f;
 #pragma unroll
