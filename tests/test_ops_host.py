@@ -218,7 +218,7 @@ def test_calls_without_rows_do_nothing(lib):
 
 def test_no_gpu_means_unsupported(lib):
     import torch
-    if torch.cuda.is_available():
+    if pytest.importorskip("torch").cuda.is_available():
         pytest.skip("GPU present")
     assert norm(lib) == cc3d.ERR_UNSUPPORTED
     assert linear(lib) == cc3d.ERR_UNSUPPORTED
@@ -238,3 +238,34 @@ def test_wrappers_refuse_tensors_off_the_device(lib):
         cc3d.attention(q, q, q, q, total=2)
     with pytest.raises((ValueError, TypeError)):
         cc3d.kv_append(q, q, q, q, total=2)
+
+
+# both caches as slices of one tensor: [n, 32, 2 heads, 64] each
+INTERLEAVED = {
+    "within heads": dict(v_cache=0x3000000 + 2 * 64, kc_head=128, kc_tok=256, kc_seq=32 * 256),
+    "within tokens": dict(v_cache=0x3000000 + 2 * 128, kc_head=64, kc_tok=256, kc_seq=32 * 256),
+    "values first": dict(v_cache=0x3000000 - 2 * 128, kc_head=64, kc_tok=256, kc_seq=32 * 256),
+    "within sequences": dict(v_cache=0x3000000 + 2 * 32 * 128, kc_head=64, kc_tok=128,
+                             kc_seq=2 * 32 * 128),
+}
+
+
+@pytest.mark.parametrize("name", INTERLEAVED)
+def test_interleaved_caches_pass_the_checks(lib, name):
+    if pytest.importorskip("torch").cuda.is_available():
+        pytest.skip("the addresses are not real")
+    kw = dict(INTERLEAVED[name])
+    kw.update({"vc_" + x: kw["kc_" + x] for x in ("seq", "tok", "head")})
+    assert append(lib, **kw) == cc3d.ERR_UNSUPPORTED  # no device: all argument checks passed
+
+
+@pytest.mark.parametrize("kw", [
+    dict(v_cache=0x3000000 + 2 * 8),                            # meeting entries
+    dict(v_cache=0x3000000 + 2 * 128),                          # a token further on
+    dict(v_cache=0x3000000 + 2 * 32 * 128),                     # the next sequence's keys
+    dict(v_cache=0x3000000 + 2 * 64, kc_head=128, kc_tok=256, kc_seq=32 * 256),  # other strides
+])
+def test_overlapping_caches_refused(lib, kw):
+    before = cc3d.cc3d_launch_count()
+    assert append(lib, **kw) == cc3d.ERR_ALIAS
+    assert cc3d.cc3d_launch_count() == before

@@ -83,11 +83,13 @@ bool strides_ok(int n, long long toks, int heads, const Strides &s) {
 }
 
 // Whether no two entries of the view share an element: ordered by stride,
-// each dimension steps over all of the smaller ones.
-bool disjoint_entries(int n, long long toks, int heads, int d, const Strides &s) {
-  long long ext[3] = {n, toks, heads}, st[3] = {s.seq, s.tok, s.head};
-  for (int i = 0; i < 2; ++i)
-    for (int j = 0; j < 2 - i; ++j)
+// each dimension steps over all of the smaller ones.  `apart` > 0: of two such
+// views, that many elements from each other.
+bool disjoint_entries(int n, long long toks, int heads, int d, const Strides &s,
+                      long long apart = 0) {
+  long long ext[4] = {n, toks, heads, apart > 0 ? 2 : 1}, st[4] = {s.seq, s.tok, s.head, apart};
+  for (int i = 0; i < 3; ++i)
+    for (int j = 0; j < 3 - i; ++j)
       if (st[j] > st[j + 1]) {
         long long t = st[j];
         st[j] = st[j + 1];
@@ -97,7 +99,7 @@ bool disjoint_entries(int n, long long toks, int heads, int d, const Strides &s)
         ext[j + 1] = t;
       }
   long long covered = d;
-  for (int i = 0; i < 3; ++i) {
+  for (int i = 0; i < 4; ++i) {
     if (ext[i] == 1) continue;
     if (st[i] < covered) return false;
     covered = (ext[i] - 1) * st[i] + covered;
@@ -326,11 +328,21 @@ cc3d_status cc3d_kv_append(const cc3d_kv_call *p, void *stream) {
       !aligned_to(p->v_cache, 16))
     return CC3D_ERR_ALIGNMENT;
   if (!disjoint_entries(p->n, ct, p->kv_heads, p->d, skc) ||
-      !disjoint_entries(p->n, ct, p->kv_heads, p->d, svc) || p->k_cache == p->v_cache)
+      !disjoint_entries(p->n, ct, p->kv_heads, p->d, svc))
     return CC3D_ERR_ALIAS;
   void *const out[2] = {p->k_cache, p->v_cache};
   const size_t ob[2] = {static_cast<size_t>(span(p->n, ct, p->kv_heads, p->d, skc)) * 2,
                         static_cast<size_t>(span(p->n, ct, p->kv_heads, p->d, svc)) * 2};
+  // the two caches may be interleaved: the same strides, and entries that do
+  // not meet
+  if (ranges_meet(out[0], ob[0], out[1], ob[1])) {
+    const bool same = (p->n == 1 || skc.seq == svc.seq) && (ct == 1 || skc.tok == svc.tok) &&
+                      (p->kv_heads == 1 || skc.head == svc.head);
+    const long long bytes = static_cast<const char *>(out[0]) - static_cast<const char *>(out[1]);
+    if (!same || bytes == 0 ||
+        !disjoint_entries(p->n, ct, p->kv_heads, p->d, skc, (bytes < 0 ? -bytes : bytes) / 2))
+      return CC3D_ERR_ALIAS;
+  }
   for (int i = 0; i < 2; ++i)
     if (ranges_meet(out[i], ob[i], p->k,
                     static_cast<size_t>(span(p->n, nt, p->kv_heads, p->d, sk)) * 2) ||
