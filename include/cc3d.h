@@ -518,8 +518,9 @@ cc3d_status cc3d_attention(const cc3d_attn_call *call, void *stream);
 
 /* The cache update that goes before cc3d_attention: the chunk's keys and
  * values ([n][t * frame][kv_heads][d] bf16) into the slots of its frames
- * (frames and slots as above; frames that the ring has no room for, the
- * chunk being longer, and frames past the last slot are not written).  The
+ * (frames and slots as above, but a count above the slots stays as it is:
+ * frames that the ring has no room for, the chunk being longer, and frames
+ * past the last slot are not written).  The
  * two caches must not overlap the inputs nor each other's entries; they may be
  * interleaved (both slices of one tensor: the same strides, at any level), else
  * CC3D_ERR_ALIAS. */

@@ -450,3 +450,17 @@ def test_no_sequences_and_no_chunk():
     cc3d.attention(c.q[:, :0], k, v, c.q[:, :0].clone(), total=4)
     cc3d.kv_append(c.q[:, :0], c.q[:, :0], k, v, total=4)
     assert cc3d.cc3d_launch_count() == before
+
+
+@pytest.mark.parametrize("ring", [0, 5])
+def test_append_with_counts_out_of_range_writes_nothing(ring):
+    """Negative counts are empty sequences, the least one among them; a frame
+    past the last slot of a plain cache has no place."""
+    counts = [-2 ** 31, -2 ** 31 + 1, -1, 0] + ([] if ring else [2 ** 31 - 1, 9])
+    n = len(counts)
+    k_frames = torch.tensor(counts, dtype=torch.int32, device="cuda")
+    new = torch.ones(n, 2, 2, 64, device="cuda", dtype=torch.bfloat16)
+    kc, vc = (torch.zeros(n, 7, 2, 64, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    cc3d.kv_append(new, new.clone(), kc, vc, sinks=2, ring=ring, k_frames=k_frames)
+    cc3d.sync_status()
+    assert not kc.any() and not vc.any()

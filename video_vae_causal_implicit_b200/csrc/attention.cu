@@ -1078,7 +1078,7 @@ __global__ void __launch_bounds__(256)
     y /= c.kv_heads;
     const int tok = static_cast<int>(y % (static_cast<long long>(c.t) * c.frame));
     const int seq = static_cast<int>(y / (static_cast<long long>(c.t) * c.frame));
-    int all = c.k_frames ? c.k_frames[seq] : c.total;
+    const int all = max(0, c.k_frames ? c.k_frames[seq] : c.total);
     int chunk = c.q_frames ? c.q_frames[seq] : c.t;
     chunk = chunk < 0 ? 0 : (chunk > c.t ? c.t : chunk);
     const int f = tok / c.frame;
