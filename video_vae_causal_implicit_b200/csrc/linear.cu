@@ -494,12 +494,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ---- few rows -----------------------------------------------------------------------
 
 constexpr int kSplitThreads = 192;
+// Shared memory of a CTA, at least: with it two of them fill an SM, and none
+// fits beside a kernel that holds all of an SM's tensor memory (those take 116
+// KB or more).  Otherwise clusters of two kernels on two streams could each
+// hold tensor memory that the other's second CTA waits for.
+constexpr size_t kSplitSmem = 112 * 1024;
 
 __host__ __device__ inline uint32_t split_total(int nt, int stages) {
   const Layout l = ring_layout(nt, stages);
   // the ring, later the partial sums [nt][128] fp32 in its place
   const uint32_t part = static_cast<uint32_t>(nt) * kTileRows * 4u;
   return (l.bars > part ? l.bars : part) + 8u * (2u * stages + 1u) + 16u;
+}
+inline size_t split_smem(int nt, int stages) {
+  const size_t used = split_total(nt, stages) + 1024;
+  return used > kSplitSmem ? used : kSplitSmem;
 }
 
 template <bool FP8>
@@ -773,7 +782,7 @@ cudaError_t prepare_kernels(int sm_count, const Prepared **out) {
           p.clusters[f][n][s] =
               s == 1 ? 2 * sm_count
                      : resident(ks[2], kSplitThreads,
-                                split_total(16 * n, split_stages(16 * n)) + 1024,
+                                split_smem(16 * n, split_stages(16 * n)),
                                 static_cast<unsigned>(s), 0);
     }
     p.done = true;
@@ -861,7 +870,7 @@ cudaError_t launch_linear(LinearArgs a, const void *x, long long ldx, const void
   if (c.split_kernel) {
     const unsigned tiles = static_cast<unsigned>(((a.n + 127) / 128) * ((a.m + c.nt - 1) / c.nt));
     const cudaLaunchConfig_t cfg =
-        launch_config(tiles * c.split, kSplitThreads, split_total(c.nt, c.stages) + 1024,
+        launch_config(tiles * c.split, kSplitThreads, split_smem(c.nt, c.stages),
                       static_cast<unsigned>(c.split), attr, stream);
     e = cudaLaunchKernelEx(&cfg, kSplit[fp8], mx, mw, a);
     count_launch();
