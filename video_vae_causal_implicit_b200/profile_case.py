@@ -27,6 +27,12 @@ Cases (seeded synthetic inputs, generated on the device):
   c4chain two c4 blocks in a row, the first one's conv2 epilogue also
           writing the second one's SiLU(RMS_norm(y)) (launches: rmsnorm,
           conv1, conv2 with the hand-over; conv1, conv2)
+  mid     the mid-block on x[1,384,5,30,52]: RMS_norm, the q, k, v product,
+          attention within each frame, the output product + x
+  ops     the transformer operators at larger sizes: 16380 rows of 4096
+          through the add + RMS norm to 8 bits; 4096 x 2048 to 8192 in E4M3
+          with GELU; 8190 tokens, 16 heads on 4, window 2048; one token of 8
+          sequences, 32 heads on 8, over a ring of 8192
 Prints nothing but a final "ok"; timing comes from the profiler.
 """
 from __future__ import annotations
@@ -44,7 +50,49 @@ def _rand(shape, dev, seed=0):
     return torch.randn(shape, generator=g, device=dev).to(torch.bfloat16)
 
 
+def build_mid(dev):
+    c, t, hw = 384, 5, 30 * 52
+    x, wqkv, wo = (_rand(shape, dev, i) for i, shape in
+                   enumerate(((t * hw, c), (3 * c, c), (c, c))))
+    wqkv, wo = wqkv * c ** -0.5, wo * c ** -0.5
+    gamma = torch.ones(c, device=dev)
+    bqkv, bo = torch.zeros(3 * c, device=dev), torch.zeros(c, device=dev)
+    a, o, y = (torch.empty_like(x) for _ in range(3))
+    qkv = torch.empty((t * hw, 3 * c), dtype=torch.bfloat16, device=dev)
+    q, k, v = (s.unflatten(1, (1, c))[None] for s in qkv.split(c, dim=1))
+
+    def run():
+        cc3d.add_rms_norm(x, gamma, y=a)
+        cc3d.linear(a, wqkv, qkv, bias=bqkv)
+        cc3d.attention(q, k, v, o.view(1, t * hw, 1, c), frame=hw, window=1, total=t)
+        cc3d.linear(o, wo, y, bias=bo, residual=x)
+    return run, []
+
+
+def build_ops(dev):
+    x, r = _rand((16380, 4096), dev, 0), _rand((16380, 4096), dev, 1)
+    h, codes = torch.empty_like(x), torch.empty_like(x, dtype=torch.float8_e4m3fn)
+    gamma, scales = torch.ones(4096, device=dev), torch.empty(16380, device=dev)
+    x8, w8 = (_rand(shape, dev, 2).to(torch.float8_e4m3fn) for shape in ((4096, 2048), (8192, 2048)))
+    sx, sw = torch.full((4096,), 0.01, device=dev), torch.full((8192,), 0.01, device=dev)
+    bias, up = torch.zeros(8192, device=dev), torch.empty((4096, 8192), dtype=torch.bfloat16, device=dev)
+    q = _rand((1, 8190, 16, 128), dev, 3)
+    k, v = (_rand((1, 8190, 4, 128), dev, i) for i in (4, 5))
+    q1 = _rand((8, 1, 32, 128), dev, 6)
+    k1, v1 = (_rand((8, 16 + 8192, 8, 128), dev, i) for i in (7, 8))
+    o, o1 = torch.empty_like(q), torch.empty_like(q1)
+
+    def run():
+        cc3d.add_rms_norm(x, gamma, residual=r, eps=1e-6, h=h, q=codes, scales=scales)
+        cc3d.linear(x8, w8, up, bias=bias, act=cc3d.ACT_GELU_TANH, x_scales=sx, w_scales=sw)
+        cc3d.attention(q, k, v, o, window=2048, sinks=4, total=8190)
+        cc3d.attention(q1, k1, v1, o1, window=8192, sinks=16, ring=8192, total=20000)
+    return run, []
+
+
 def build_case(name, dev):
+    if name in ("mid", "ops"):
+        return build_mid(dev) if name == "mid" else build_ops(dev)
     if name in ("c2", "c2s", "c2c"):
         c, T, H, W = 384, 5, 30, 52
     elif name == "c3a":
