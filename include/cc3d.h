@@ -497,8 +497,9 @@ cc3d_status cc3d_linear(const cc3d_linear_call *call, void *stream);
  * are).  heads is a multiple of kv_heads; query head h reads kv head
  * h / (heads / kv_heads).  scale 0 stands for 1 / sqrt(d).
  *
- * One kernel launch, no workspace; the same arguments give the same bytes on
- * every call.  d % 8 == 0, d <= 384, heads / kv_heads <= 128, at most 2^31 -
+ * One kernel launch (or two, where that splits a long chunk of one frame
+ * better), no workspace; the same arguments give the same bytes on every call.
+ * d % 8 == 0, d <= 384, heads / kv_heads <= 128, at most 2^31 -
  * 1024 tokens in q or in a cache, n and kv_heads <= 65535, else
  * CC3D_ERR_UNSUPPORTED.  o must not
  * overlap an input's extent, nor its own rows (CC3D_ERR_ALIAS).  n = 0 and

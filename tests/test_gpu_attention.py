@@ -464,3 +464,35 @@ def test_append_with_counts_out_of_range_writes_nothing(ring):
     cc3d.kv_append(new, new.clone(), kc, vc, sinks=2, ring=ring, k_frames=k_frames)
     cc3d.sync_status()
     assert not kc.any() and not vc.any()
+
+
+# One frame a call, long enough for whole waves of full row tiles and a second
+# launch for what is left: (least launches, the case)
+LONG_FRAMES = {
+    "ring with sink": (2, dict(frame=1560, total=9, d=128, heads=12, kv=12, window=6, sinks=1,
+                               ring=6)),
+    "many heads": (2, dict(frame=1560, total=9, d=128, heads=24, kv=24, window=4, sinks=1,
+                           ring=4)),
+    "shared heads": (1, dict(frame=1301, total=7, d=64, heads=24, kv=8, window=5, sinks=1)),
+    "odd head size": (1, dict(frame=1811, total=6, d=200, heads=6, kv=6)),
+    "lengths and padding": (1, dict(n=3, frame=1560, d=128, heads=12, kv=12, window=4, sinks=2,
+                                    ring=4, k_frames=[9, 1, 4], q_frames=[1, 1, 0])),
+}
+
+
+@pytest.mark.parametrize("name", LONG_FRAMES)
+def test_long_frame_in_two_launches(name):
+    launches, kw = LONG_FRAMES[name]
+    c = Case(**kw, seed=len(name))
+    k, v = c.caches()
+    before = cc3d.cc3d_launch_count()
+    o = c.run(k=k, v=v)
+    assert launches <= cc3d.cc3d_launch_count() - before <= 2
+    c.check(o)
+    again = torch.full_like(o, 7.0)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cc3d.attention(c.q, k, v, again, **c.args())
+    graph.replay()
+    cc3d.sync_status()
+    assert torch.equal(o, again)

@@ -26,8 +26,8 @@
 // Bound: the tensor pipe and the exponentials (16 a cycle and SM, as many
 // cycles as the two products take at d = 128) for many rows, the cache's
 // bytes for one token.  Measured: 8190 tokens, 16 heads on 4 of d = 128, window
-// 2048 and 4 sinks 124 us (970 TFLOP/s; a step of 64 keys takes a CTA's 256
-// rows about 1700 cycles, of which the products want 1130 and the exponentials
+// 2048 and 4 sinks 122 us (990 TFLOP/s; a step of 64 keys takes a CTA's 256
+// rows about 1670 cycles, of which the products want 1130 and the exponentials
 // 1024); frames of 1560 tokens, d = 384, within themselves 31 us for five; one
 // token of 8 sequences, 32 heads on 8, over 8208 cached 47 us (5.7 TB/s).
 #include <cuda_bf16.h>
@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(attn_threads(NQ), OCC)
     up = p.by_n.quotient(i);
     seq = i - up * cs.n;
     // the last query tiles see the most keys: first
-    const int tile = p.q_tiles - 1 - up;
+    const int tile = p.tile0 + p.q_tiles - 1 - up;
     int chunk, all;
     lengths(cs, seq, chunk, all);
     base = all - chunk;  // frame of query token 0 (negative: sees nothing)
@@ -805,7 +805,7 @@ __global__ void __launch_bounds__(attn_threads(NQ), OCC)
       uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
       for (int i = 0; i < KT; i += 32) {
-        uint32_t w[16];
+        uint32_t *w = raw + i / 2;  // (the weights take the scores' registers)
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
           const float2 x = unpair(pair_fma(
@@ -814,13 +814,15 @@ __global__ void __launch_bounds__(attn_threads(NQ), OCC)
           sum[(e / 2) & 1] = pair_add(sum[(e / 2) & 1], pair_of(a, b));
           w[e / 2] = pack_bf16x2(a, b);
         }
-        tmem_st16(sc + i / 2, w);
       }
       {
         const float2 x = unpair(pair_add(sum[0], sum[1]));
         l += x.x + x.y;
       }
+      // (stores within the turn: 130.5 us where this takes 127.9, at 8190 tokens)
       pass_turn(j);
+#pragma unroll
+      for (int i = 0; i < KT / 2; i += 16) tmem_st16(sc + i, raw + i);
       tmem_wait_st();
       if (masked) {
         ok = await(v_clean, static_cast<uint32_t>(n_masked++) & 1u, 37);
@@ -1236,70 +1238,129 @@ cudaError_t launch_attention(AttnArgs a, const void *q, const Strides &sq, const
     return across;
   };
   const long long have = c.k_frames || c.ring > 0 ? c.slots : c.total;  // frames there are
-  // Candidates: two row tiles a CTA (d <= 128: a key tile is read once for
-  // both, and one's softmax runs under the other's products), one, or one and
-  // two CTAs an SM; keys split over 1 to 8 CTAs of a cluster.  The least time
-  // by the cycles that a key tile's steps, a CTA's start and end, and the
-  // joining of the parts were measured to take (d = 64 to 384, 1 to 8190
-  // queries, 500 to 20000 keys), over whole waves of what fits at once.
-  double best = 1e300;
-  long long q_tiles = 0;
-  const Variant *pick = nullptr;
-  for (const Variant &v : variants()) {
-    if (c.d > v.d_most || c.d <= v.d_above) continue;
-    int per_frame = 0;
-    const long long tiles = tile_count(v.nq, &per_frame);
-    if (tiles * heads > INT32_MAX / 8) continue;
-    // key tiles of a query tile (its first frame's window and what its later
-    // frames add)
+  // A launch: two row tiles a CTA (d <= 128: a key tile is read once for both,
+  // and one's softmax runs under the other's products), one, or one and two
+  // CTAs an SM; keys split over 1 to 8 CTAs of a cluster.
+  struct Launch {
+    const Variant *kernel;
+    int split, per_frame;
+    long long tiles;
+    double time;
+  };
+  // key tiles of a query tile (its first frame's window and what its later
+  // frames add)
+  auto key_tiles = [&](const Variant &v, int per_frame) {
     const long long span =
         per_frame > 0 ? 1 : (static_cast<long long>(v.nq) * a.tok_tile - 1) / c.frame + 1;
     const long long frames = seen + (span < c.t ? span : c.t) - 1;
     const long long keys = (frames < have ? frames : have) * c.frame;
-    const double steps = static_cast<double>((keys + v.kt - 1) / v.kt);
-    for (int split = 1; split <= 8 && split <= steps; ++split) {
-      const int fit = prepared->fit[&v - variants()][split];
-      if (fit < 1) continue;
-      // (a few waves are whole ones; the last of many overlaps the others')
-      const double parts = static_cast<double>(tiles * heads) / fit;
-      const double waves = parts < 4.0 ? std::ceil(parts) : parts + 0.5;
-      // (alone on its SM a CTA of a pair steps faster)
-      const double step = v.occ == 2 && tiles * heads * split <= sm_count ? 0.85 * v.step : v.step;
-      const double join = split > 1 ? 3000.0 + 30.0 * v.nq * c.d : 0.0;
-      const double t = waves * (std::ceil(steps / split) * step + 7000.0 + 20.0 * c.d + join);
-      if (t < best) {
-        best = t;
-        pick = &v;
-        q_tiles = tiles;
-        a.split = split;
-        a.tiles_frame = per_frame;
+    return static_cast<double>((keys + v.kt - 1) / v.kt);
+  };
+  // Cycles that a key tile's steps, a CTA's start and end, and the joining of
+  // the parts were measured to take (d = 64 to 384, 1 to 8190 queries, 500 to
+  // 20000 keys), of `waves` whole waves of what fits at once.
+  auto time_of = [&](const Variant &v, double steps, int split, double waves, double step) {
+    const double join = split > 1 ? 3000.0 + 30.0 * v.nq * c.d : 0.0;
+    return waves * (std::ceil(steps / split) * step + 7000.0 + 20.0 * c.d + join);
+  };
+  // The fastest single launch for all query tokens, or those from the first
+  // `skip` on (skip > 0 with t = 1 only).
+  auto fastest = [&](long long skip) {
+    Launch best = {nullptr, 1, 0, 0, 1e300};
+    for (const Variant &v : variants()) {
+      if (c.d > v.d_most || c.d <= v.d_above) continue;
+      const long long rows = static_cast<long long>(v.nq) * a.tok_tile;
+      if (skip % rows != 0) continue;
+      int per_frame = 0;
+      const long long tiles = tile_count(v.nq, &per_frame) - skip / rows;
+      if (tiles * heads > INT32_MAX / 8) continue;
+      const double steps = key_tiles(v, per_frame);
+      for (int split = 1; split <= 8 && split <= steps; ++split) {
+        const int fit = prepared->fit[&v - variants()][split];
+        if (fit < 1) continue;
+        // (a few waves are whole ones; the last of many overlaps the others')
+        const double parts = static_cast<double>(tiles * heads) / fit;
+        const double waves = parts < 4.0 ? std::ceil(parts) : parts + 0.5;
+        // (alone on its SM a CTA of a pair steps faster)
+        const double step =
+            v.occ == 2 && tiles * heads * split <= sm_count ? 0.85 * v.step : v.step;
+        const double t = time_of(v, steps, split, waves, step);
+        if (t < best.time) best = {&v, split, per_frame, tiles, t};
+      }
+    }
+    return best;
+  };
+  Launch parts[2] = {fastest(0), {}};
+  if (!parts[0].kernel) return cudaErrorInvalidValue;
+  int n_parts = 1;
+  // The queries of one frame, of which all see the same keys, may also go in
+  // two launches: whole waves of full tiles, and what is left with more CTAs a
+  // tile.  (A frame of 1560 tokens, 12 heads of 128, over 7 frames: 84 pairs of
+  // row tiles are more than half of the SMs, and 12 of them nearly empty: 134
+  // us in one launch, 120 in two; 24 heads 259 and 207; a frame of 6240, 4
+  // heads, over 5 frames 410 and 360.)  Looked for where a call is long enough
+  // to hide the search.
+  if (c.t == 1 && parts[0].time > 80000.0) {
+    // (a second launch costs some 4000 cycles; a gain of 3 % or less is within
+    // the estimate's error)
+    double least = 0.97 * parts[0].time - 4000.0;
+    for (const Variant &v : variants()) {
+      if (c.d > v.d_most || c.d <= v.d_above) continue;
+      const long long rows = static_cast<long long>(v.nq) * a.tok_tile;
+      const double steps = key_tiles(v, 0);
+      for (int split = 1; split <= 8 && split <= steps; ++split) {
+        const int fit = prepared->fit[&v - variants()][split];
+        for (int waves = 1; waves <= 3; ++waves) {
+          long long tiles = static_cast<long long>(waves) * fit / heads;
+          if (tiles > tokens / rows) tiles = tokens / rows;
+          if (tiles < 1 || tiles * rows >= tokens || tiles * heads > INT32_MAX / 8) continue;
+          const double first = time_of(v, steps, split, waves, v.step);
+          if (first >= least) break;
+          const Launch rest = fastest(tiles * rows);
+          if (rest.kernel && first + rest.time < least) {
+            least = first + rest.time;
+            parts[0] = {&v, split, 0, tiles, first};
+            parts[1] = rest;
+            n_parts = 2;
+          }
+        }
       }
     }
   }
-  if (!pick) return cudaErrorInvalidValue;
-  const int kt = pick->kt;
-  a.q_tiles = static_cast<int>(q_tiles);
   a.by_frame = FastDiv(static_cast<uint32_t>(c.frame));
   a.by_group = FastDiv(static_cast<uint32_t>(a.group));
   a.by_kv = FastDiv(static_cast<uint32_t>(c.kv_heads));
   a.by_n = FastDiv(static_cast<uint32_t>(c.n));
-  a.by_split = FastDiv(static_cast<uint32_t>(a.split));
   a.by_ring = FastDiv(static_cast<uint32_t>(c.ring > 0 ? c.ring : 1));
-  a.by_tiles_frame = FastDiv(static_cast<uint32_t>(a.tiles_frame > 0 ? a.tiles_frame : 1));
-  const long long grid = q_tiles * heads * a.split;
-  if (grid > INT32_MAX) return cudaErrorInvalidValue;
-  CUtensorMap mq, mk, mv;
+  CUtensorMap mq;
   const long long cached = static_cast<long long>(c.slots) * c.frame;
-  if (!encode_heads(&mq, q, c.d, a.heads, tokens, c.n, sq, a.group, a.tok_tile) ||
-      !encode_heads(&mk, k, c.d, c.kv_heads, cached, c.n, sk, 1, kt) ||
-      !encode_heads(&mv, v, c.d, c.kv_heads, cached, c.n, sv, 1, kt))
+  if (!encode_heads(&mq, q, c.d, a.heads, tokens, c.n, sq, a.group, a.tok_tile))
     return cudaErrorInvalidValue;
-  cudaLaunchAttribute attr[2];
-  const cudaLaunchConfig_t cfg =
-      launch_config(*pick, static_cast<unsigned>(grid), a.split, attr, stream);
-  e = cudaLaunchKernelEx(&cfg, pick->kernel, mq, mk, mv, static_cast<const AttnArgs>(a));
-  count_launch();
-  return e;
+  long long first_row = 0;  // query tokens of the launch before
+  for (int i = 0; i < n_parts; ++i) {
+    const Variant &v0 = *parts[i].kernel;
+    const long long rows = static_cast<long long>(v0.nq) * a.tok_tile;
+    a.q_tiles = static_cast<int>(parts[i].tiles);
+    a.tile0 = static_cast<int>(first_row / rows);
+    first_row = parts[i].tiles * rows;
+    a.split = parts[i].split;
+    a.tiles_frame = parts[i].per_frame;
+    a.by_split = FastDiv(static_cast<uint32_t>(a.split));
+    a.by_tiles_frame = FastDiv(static_cast<uint32_t>(a.tiles_frame > 0 ? a.tiles_frame : 1));
+    const long long grid = parts[i].tiles * heads * a.split;
+    if (grid > INT32_MAX) return cudaErrorInvalidValue;
+    CUtensorMap mk, mv;
+    if (!encode_heads(&mk, k, c.d, c.kv_heads, cached, c.n, sk, 1, v0.kt) ||
+        !encode_heads(&mv, v, c.d, c.kv_heads, cached, c.n, sv, 1, v0.kt))
+      return cudaErrorInvalidValue;
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg =
+        launch_config(v0, static_cast<unsigned>(grid), a.split, attr, stream);
+    e = cudaLaunchKernelEx(&cfg, v0.kernel, mq, mk, mv, static_cast<const AttnArgs>(a));
+    if (e != cudaSuccess) return e;
+    count_launch();
+  }
+  return cudaSuccess;
 }
 
 cudaError_t launch_kv_append(const CacheShape &c, const __nv_bfloat16 *k, const Strides &sk,

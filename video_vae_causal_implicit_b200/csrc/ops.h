@@ -110,9 +110,9 @@ struct AttnArgs {
   int *status;
   unsigned long long wait_limit_ns;
   int group, tok_tile;     // query heads per kv head; tokens per 128 rows
-  // set by launch_attention; tiles_frame: query tiles of a frame, 0 where tiles
+  // set by launch_attention; tile0: the launch's first query tile; tiles_frame: query tiles of a frame, 0 where tiles
   // cross frames
-  int split, q_tiles, tiles_frame;
+  int split, q_tiles, tile0, tiles_frame;
   FastDiv by_frame, by_group, by_kv, by_n, by_split, by_ring, by_tiles_frame;
 };
 struct Strides {
