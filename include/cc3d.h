@@ -450,7 +450,8 @@ cc3d_status cc3d_add_rms_norm(const cc3d_add_norm_call *call, void *stream);
  *   (the other NULL / 0); CC3D_BF16: all of them NULL / 0.
  * x, weight, y, residual, bias and w_scales 16-byte aligned.  k, ldx, ldw
  * multiples of 8 (bf16) or 16 (E4M3); n, ldy, ldr multiples of 8; m, n, k and
- * row distances at most 2^30, else CC3D_ERR_UNSUPPORTED.  m = 0 does nothing.
+ * row distances at most 2^30, y at most 2^30 tiles of 128 x 64, else
+ * CC3D_ERR_UNSUPPORTED.  m = 0 does nothing.
  * One kernel launch; the same arguments give the same bytes on every call. */
 typedef struct {
   const void *x, *weight;
@@ -499,11 +500,10 @@ cc3d_status cc3d_linear(const cc3d_linear_call *call, void *stream);
  *
  * One kernel launch (or two, where that splits a long chunk of one frame
  * better), no workspace; the same arguments give the same bytes on every call.
- * d % 8 == 0, d <= 384, heads / kv_heads <= 128, at most 2^31 -
- * 1024 tokens in q or in a cache, n and kv_heads <= 65535, else
- * CC3D_ERR_UNSUPPORTED.  o must not
- * overlap an input's extent, nor its own rows (CC3D_ERR_ALIAS).  n = 0 and
- * t = 0 do nothing. */
+ * d % 8 == 0, d <= 384, heads / kv_heads <= 128, at most 2^31 - 1024 tokens
+ * in q or in a cache, n and kv_heads <= 65535, n * kv_heads * (tiles of 128
+ * query rows) < 2^28, else CC3D_ERR_UNSUPPORTED.  o must not overlap an input's
+ * extent, nor its own rows (CC3D_ERR_ALIAS).  n = 0 and t = 0 do nothing. */
 typedef struct {
   int n, heads, kv_heads, d;
   int frame, t, slots, window, sinks, ring;
@@ -521,10 +521,9 @@ cc3d_status cc3d_attention(const cc3d_attn_call *call, void *stream);
  * values ([n][t * frame][kv_heads][d] bf16) into the slots of its frames
  * (frames and slots as above, but a count above the slots stays as it is:
  * frames that the ring has no room for, the chunk being longer, and frames
- * past the last slot are not written).  The
- * two caches must not overlap the inputs nor each other's entries; they may be
- * interleaved (both slices of one tensor: the same strides, at any level), else
- * CC3D_ERR_ALIAS. */
+ * past the last slot are not written).  The two caches must not overlap the
+ * inputs nor each other's entries; they may be interleaved (both slices of one
+ * tensor: the same strides, at any level), else CC3D_ERR_ALIAS. */
 typedef struct {
   int n, kv_heads, d, frame, t, slots, sinks, ring;
   int total;   /* ignored with k_frames */

@@ -496,3 +496,16 @@ def test_long_frame_in_two_launches(name):
     graph.replay()
     cc3d.sync_status()
     assert torch.equal(o, again)
+
+
+def test_more_tiles_than_a_grid_holds_are_refused():
+    """2^32 heads of all sequences: refused before an address is looked at."""
+    n = 65535
+    seq, far = n * 8, 1 << 40
+    names = ("n heads kv_heads d frame t slots window sinks ring total scale q_frames k_frames q k v "
+             "o").split()
+    a = dict(zip(names, (n, n, n, 8, 1, 1, 1, 0, 0, 0, 1, 0.0, 0, 0, far, 2 * far, 3 * far, 4 * far)))
+    before = cc3d.cc3d_launch_count()
+    call = cc3d._ATTN_CALL.pack(*a.values(), *(4 * (seq, seq, 8)))
+    assert cc3d.lib().cc3d_attention(call, None) == cc3d.ERR_UNSUPPORTED
+    assert cc3d.cc3d_launch_count() == before

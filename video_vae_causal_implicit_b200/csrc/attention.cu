@@ -1291,7 +1291,7 @@ cudaError_t launch_attention(AttnArgs a, const void *q, const Strides &sq, const
     return best;
   };
   Launch parts[2] = {fastest(0), {}};
-  if (!parts[0].kernel) return cudaErrorInvalidValue;
+  if (!parts[0].kernel) return cudaErrorNotSupported;  // (too many tiles for a grid)
   int n_parts = 1;
   // The queries of one frame, of which all see the same keys, may also go in
   // two launches: whole waves of full tiles, and what is left with more CTAs a
@@ -1348,7 +1348,7 @@ cudaError_t launch_attention(AttnArgs a, const void *q, const Strides &sq, const
     a.by_split = FastDiv(static_cast<uint32_t>(a.split));
     a.by_tiles_frame = FastDiv(static_cast<uint32_t>(a.tiles_frame > 0 ? a.tiles_frame : 1));
     const long long grid = parts[i].tiles * heads * a.split;
-    if (grid > INT32_MAX) return cudaErrorInvalidValue;
+    if (grid > INT32_MAX) return cudaErrorNotSupported;
     CUtensorMap mk, mv;
     if (!encode_heads(&mk, k, c.d, c.kv_heads, cached, c.n, sk, 1, v0.kt) ||
         !encode_heads(&mv, v, c.d, c.kv_heads, cached, c.n, sv, 1, v0.kt))

@@ -889,7 +889,7 @@ cudaError_t launch_linear(LinearArgs a, const void *x, long long ldx, const void
   a.m_tiles = (a.m + rows - 1) / rows;
   a.n_tiles = (a.n + c.nt - 1) / c.nt;
   const long long tiles = static_cast<long long>(a.m_tiles) * a.n_tiles;
-  if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
+  if (tiles > INT32_MAX / 2) return cudaErrorNotSupported;
   a.by_band = FastDiv(static_cast<uint32_t>(kBand * a.n_tiles));
   a.by_last = FastDiv(static_cast<uint32_t>(a.m_tiles % kBand ? a.m_tiles % kBand : kBand));
   const long long slots = c.pair ? pre->pairs[fp8] : sm_count;

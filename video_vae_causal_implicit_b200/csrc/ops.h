@@ -23,6 +23,7 @@ inline bool ranges_meet(const void *a, size_t na, const void *b, size_t nb) {
 inline cc3d_status status_of(cudaError_t e) {
   return e == cudaSuccess ? CC3D_OK
          : e == cudaErrorMemoryAllocation ? CC3D_ERR_OOM
+         : e == cudaErrorNotSupported     ? CC3D_ERR_UNSUPPORTED
                                           : CC3D_ERR_CUDA;
 }
 
