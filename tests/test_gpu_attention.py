@@ -509,3 +509,21 @@ def test_more_tiles_than_a_grid_holds_are_refused():
     call = cc3d._ATTN_CALL.pack(*a.values(), *(4 * (seq, seq, 8)))
     assert cc3d.lib().cc3d_attention(call, None) == cc3d.ERR_UNSUPPORTED
     assert cc3d.cc3d_launch_count() == before
+
+
+@pytest.mark.parametrize("heads,kv,total", [(8, 1, 4000), (16, 2, 9000), (4, 4, 130)])
+@pytest.mark.parametrize("spread", [1.0, 30.0, 4000.0])
+def test_one_token_with_scores_over_the_whole_range(heads, kv, total, spread):
+    """Weights from 1 down to below the least number (scores apart by more than
+    2^7 and 2^12), and a NaN score in every place of a key tile in turn."""
+    c = Case(total=total, d=64, heads=heads, kv=kv, seed=total)
+    c.check(c.run(scale=spread * 64 ** -0.5), spread * 64 ** -0.5)
+    if spread == 1.0:
+        k, v = c.caches()
+        for key in list(range(total - 128, total)):
+            kn = k.clone()
+            kn[0, key, 0, 3] = float("nan")
+            o = c.run(k=kn, v=v)
+            mine = o[0, 0, :heads // kv].float()
+            assert torch.isnan(mine).all(), key
+            assert torch.isfinite(o[0, 0, heads // kv:].float()).all(), key

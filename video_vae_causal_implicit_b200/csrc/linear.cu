@@ -71,11 +71,6 @@ __device__ __forceinline__ float rcp_approx(float x) {
 //    to erfcx(x) / 2t for t in (0, 1]: relative error 6e-7 in fp32.  |a| counts
 //    as 64 at most (h is 0 there, and +-inf give their limits).
 // NaN stays NaN and leaves the pair's other value alone.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float y;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-  return y;
-}
 // a / (1 + 2^z)
 __device__ __forceinline__ uint64_t over_one_plus_exp2(uint64_t a, uint64_t z) {
   const float2 e = unpair(z), f = unpair(a);

@@ -617,6 +617,13 @@ __device__ __forceinline__ void regs_more() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// The larger one; NaN where either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
 // ---- packed fp32 pairs: two lanes of math per instruction -------------------------
 __device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
   uint64_t r;
