@@ -527,3 +527,27 @@ def test_one_token_with_scores_over_the_whole_range(heads, kv, total, spread):
             mine = o[0, 0, :heads // kv].float()
             assert torch.isnan(mine).all(), key
             assert torch.isfinite(o[0, 0, heads // kv:].float()).all(), key
+
+
+def test_counts_out_of_range_count_as_the_nearest():
+    """Frame counts below 0 or above the slots, chunk counts below 0 or above
+    t; in a ring, the largest count there is."""
+    top = 2 ** 31 - 1
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rnd = lambda *s: torch.randn(*s, device="cuda", generator=g).to(torch.bfloat16)  # noqa: E731
+    ints = lambda *x: torch.tensor(x, device="cuda", dtype=torch.int32)  # noqa: E731
+    q, k, v = rnd(4, 2, 4, 64), rnd(4, 12, 2, 64), rnd(4, 12, 2, 64)
+
+    def run(counts, chunks, **kw):
+        o = torch.full_like(q, 7.0)
+        cc3d.attention(q, k, v, o, k_frames=ints(*counts), q_frames=ints(*chunks), **kw)
+        cc3d.sync_status()
+        return o
+    o = run((-2 ** 31, -1, top, 13), (2, 99, top, -3), window=5, sinks=1)
+    assert torch.equal(o, run((0, 0, 12, 12), (2, 2, 2, 0), window=5, sinks=1))
+    assert (o[:2] == 0).all() and (o[3] == 7).all()
+    # of frames 2, 3, ... one in ten has the same slot
+    ring = dict(window=8, sinks=2, ring=10)
+    same = [2 + (x - 2) % 10 + 20 for x in (top, top - 1, top - 9)]
+    o = run((top, top - 1, top - 9, -7), (2, 2, 1, 2), **ring)
+    assert torch.equal(o, run((*same, 0), (2, 2, 1, 2), **ring))
