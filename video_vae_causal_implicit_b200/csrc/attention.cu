@@ -187,7 +187,13 @@ struct Shape {
   }
   static constexpr int kStages = stages();
   static constexpr uint32_t kBars = kQ + kStages * kGroup;
-  static constexpr uint32_t kSmem = kBars + rest(kStages);
+  // (Of two CTAs an SM 112 KB at least: none then fits beside a kernel that
+  // holds all of an SM's tensor memory, which takes 116 KB or more.  Otherwise
+  // clusters of two kernels on two streams could each hold tensor memory that
+  // the other's second CTA waits for.)
+  static constexpr uint32_t kUsed = kBars + rest(kStages);
+  static constexpr uint32_t kSmem = OCC > 1 && kUsed < 112 * 1024 ? 112 * 1024 : kUsed;
+  static_assert(OCC == 1 || (kSmem + 1024) * OCC <= 228 * 1024, "CTAs of an SM");
   // tensor memory: two slots of scores and the output per row tile
   static constexpr uint32_t kTmemCols = 512 / OCC;
   static_assert(2 * NQ * KT + NQ * 64 * CH <= static_cast<int>(kTmemCols), "tensor memory columns");
