@@ -185,3 +185,45 @@ def test_norm_codes_feed_an_fp8_conv_plan():
     ref = oracle.causal_conv3d(synth.ncthw_view(xv), wv, case["b"].double().numpy())
     assert_close_bf16(ncthw_np(y), ref, "norm codes into an FP8 conv")
     plan.close()
+
+
+def test_calls_on_several_streams_at_once():
+    """Products, attentions and convs on streams of their own give the bytes
+    that each gives alone (clusters of different kernels then share the SMs)."""
+    x1, w1 = rnd(1, 2048, seed=1), rnd(12288, 2048, seed=2, std=2048 ** -0.5)
+    x2, w2 = rnd(7800, 384, seed=3), rnd(1152, 384, seed=4, std=384 ** -0.5)
+    qf, kf, vf = (rnd(1, 1560, 12, 128, seed=s) for s in (5, 6, 7))
+    qt, kt, vt = rnd(4, 1, 32, 64, seed=8), rnd(4, 3000, 8, 64, seed=9), rnd(4, 3000, 8, 64, seed=10)
+    xc = rnd(1, 5, 30, 52, 384, seed=11)
+    plan = cc3d.Plan(rnd(384, 384, 3, 3, 3, seed=12, std=0.01), torch.zeros(384, device="cuda"), h=30,
+                     w=52, max_t=5)
+
+    def new(*shape):
+        return torch.empty(shape, device="cuda", dtype=torch.bfloat16)
+
+    def conv():
+        y = new(1, 5, 30, 52, 384)
+        plan.forward(xc, y)
+        return y
+
+    calls = [
+        lambda: cc3d.linear(x1, w1, new(1, 12288), act=cc3d.ACT_SILU),
+        lambda: cc3d.attention(qf, kf, vf, new(1, 1560, 12, 128), frame=1560, total=1),
+        conv,
+        lambda: cc3d.linear(x2, w2, new(7800, 1152)),
+        lambda: cc3d.attention(qt, kt, vt, new(4, 1, 32, 64), total=3000),
+    ]
+    alone = [f() for f in calls]
+    cc3d.sync_status()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(20):
+        got = []
+        for i, s in enumerate(streams):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                for j in (i, (i + 2) % len(calls)):
+                    got.append((j, calls[j]()))
+        torch.cuda.synchronize()
+        for j, o in got:
+            assert torch.equal(o, alone[j]), j
+    cc3d.sync_status()
