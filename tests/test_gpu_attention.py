@@ -551,3 +551,57 @@ def test_counts_out_of_range_count_as_the_nearest():
     same = [2 + (x - 2) % 10 + 20 for x in (top, top - 1, top - 9)]
     o = run((top, top - 1, top - 9, -7), (2, 2, 1, 2), **ring)
     assert torch.equal(o, run((*same, 0), (2, 2, 1, 2), **ring))
+
+
+# Few query rows over many keys (their keys are split over a cluster), and many
+# rows, whose keys are not: NaN has to come out of both alike.
+NAN_SCORES = {
+    "token long": dict(total=9000, d=128, heads=4, kv=1),
+    "token": dict(n=3, total=2100, d=64, heads=8, kv=2),
+    "token odd head size": dict(total=4100, d=80, heads=4, kv=4),
+    "tokens": dict(t=4, total=3001, d=128, heads=8, kv=2),
+    "ring": dict(total=9003, d=128, heads=8, kv=2, window=2000, sinks=5, ring=2000),
+    "frames": dict(frame=1560, t=5, total=5, d=384, window=1),
+    "wide frame": dict(frame=700, t=1, total=3, d=200, heads=2, kv=2),
+    "stream": dict(frame=500, t=1, total=9, d=128, heads=2, kv=2, window=6, sinks=1, ring=6),
+    "unsplit": dict(t=1500, total=1500, d=128, heads=48, kv=16, window=333, sinks=5),
+    "unsplit frames": dict(frame=200, t=4, total=6, d=64, heads=20, kv=20, window=3, sinks=1),
+}
+
+
+@pytest.mark.parametrize("name", NAN_SCORES)
+def test_nan_queries_and_runs_of_nan_keys_are_as_in_the_definition(name):
+    """A query with a NaN has no finite output, and neither has one that sees a
+    NaN key, also where every key of a long run of keys (longer than what one
+    of eight CTAs may take) is NaN; all other outputs stay."""
+    c = Case(**NAN_SCORES[name], seed=5)
+    nan = float("nan")
+    c.check(c.run())
+    # NaN queries: one row of a head, and a whole token
+    rows = c.q.shape[1]
+    c.q[0, 0, c.heads - 1, 3] = nan
+    c.q[c.n - 1, rows - 1, :, c.d - 1] = nan
+    assert _check_with_nan(c, c.run()) > 0
+    c.q.nan_to_num_(0.5)
+    # runs of NaN keys of one kv head: short, a third, all but the last and all
+    most, odd = c.all[0] * c.f, 0
+    for lo, hi in ((most // 2, most // 2 + 1), (most // 3, 2 * most // 3), (0, most - 1),
+                   (1, most), (0, most)):
+        kept = c.lk[0, lo:hi, c.kv - 1].clone()
+        c.lk[0, lo:hi, c.kv - 1, 1] = nan
+        odd += _check_with_nan(c, c.run())
+        c.lk[0, lo:hi, c.kv - 1] = kept
+    assert odd > 0  # (a window may hide some of the runs)
+
+
+def _check_with_nan(c, o):
+    odd = 0
+    for b in range(c.n):
+        ref, tol = c.reference(b)
+        got = o[b, :ref.shape[0]].double()
+        odd += int(torch.isnan(ref).sum())
+        assert torch.equal(torch.isnan(got), torch.isnan(ref)), (
+            b, (torch.isnan(got) != torch.isnan(ref)).nonzero()[:4].tolist())
+        good = torch.isnan(ref) | ((got - ref).abs() <= tol)
+        assert good.all(), (b, (~good).nonzero()[:3].tolist())
+    return odd

@@ -1039,17 +1039,20 @@ __global__ void __launch_bounds__(attn_threads(NQ), OCC)
 #pragma unroll
       for (int k = 0; k < 8; ++k)
         if (k < split) top = fmaxf(top, of[k].x);
+      // A rank has nothing of the row where its sum is 0.  (A maximum of -inf
+      // does not say so: maxima pass over NaN, so it is that of a rank whose
+      // scores are all NaN too; its sum is NaN then, and so is the row.)
       float all = 0.f;
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (k < split && of[k].x != -INFINITY)
+        if (k < split && of[k].y != 0.f)
           all += of[k].y * exp2_fast((of[k].x - top) * p.scale_log2);
       const float2 me = row_ml[wg * kRows + r];
       float f = 0.f;
-      if (me.x != -INFINITY && (all > 0.f || all != all))
-        f = exp2_fast((me.x - top) * p.scale_log2) / all;
+      if (me.y != 0.f) f = exp2_fast((me.x - top) * p.scale_log2) / all;
       const uint32_t o = o_col + wg * o_cols + (static_cast<uint32_t>((warp % 4) * 32) << 16);
-      const bool have = ok && nj > 0;
+      const bool have = ok && nj > 0;  // (the same in every lane)
+      const bool some = have && me.y != 0.f;
       float *dst = part + (wg * kRows + r) * pitch;
 #pragma unroll 1
       for (int i = 0; i < cs.d; i += 32) {
@@ -1062,7 +1065,7 @@ __global__ void __launch_bounds__(attn_threads(NQ), OCC)
         }
 #pragma unroll
         for (int e = 0; e < 32; ++e)
-          v[e] = (have && f != 0.f) ? __float_as_uint(__uint_as_float(v[e]) * f) : 0u;
+          v[e] = some ? __float_as_uint(__uint_as_float(v[e]) * f) : 0u;
         if (r < tile_rows) {
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
