@@ -605,3 +605,31 @@ def _check_with_nan(c, o):
         good = torch.isnan(ref) | ((got - ref).abs() <= tol)
         assert good.all(), (b, (~good).nonzero()[:3].tolist())
     return odd
+
+
+@pytest.mark.parametrize("name", NAN_SCORES)
+def test_scores_of_minus_infinity(name):
+    """Keys with a score of -inf have no weight; a query that sees only such keys
+    has no value (NaN), unlike one that sees nothing (zeros)."""
+    c = Case(**NAN_SCORES[name], seed=6)
+    c.q[..., 2] = c.q[..., 2].abs() + 0.5
+    most, group, plain, odd = c.all[0] * c.f, c.heads // c.kv, c.seen, 0
+    for lo, hi in ((most // 3, 2 * most // 3), (0, most - 1), (1, most), (0, most)):
+        kept = c.lk[0, lo:hi, c.kv - 1].clone()
+        c.lk[0, lo:hi, c.kv - 1, 2] = -math.inf
+        o = c.run()[0, :c.chunk[0] * c.f].double()
+        run = torch.zeros(most, device="cuda", dtype=torch.bool)
+        run[lo:hi] = True
+        c.seen = lambda b: plain(b) & ~run
+        left, seen = c.seen(0), plain(0)
+        none = seen.any(1) & ~left.any(1)
+        odd += int(none.sum())
+        ref, tol = c.reference(0)
+        c.seen = plain
+        mine = slice((c.kv - 1) * group, c.heads)  # the heads that read these keys
+        assert torch.isnan(o[none][:, mine]).all(), (lo, hi)
+        assert ((o - ref).abs() <= tol)[~none][:, mine].all(), (lo, hi)
+        c.lk[0, lo:hi, c.kv - 1] = kept
+    assert odd > 0
+    blank = Case(**dict(NAN_SCORES[name], k_frames=[0] * c.n), seed=6)
+    assert (blank.run() == 0).all()

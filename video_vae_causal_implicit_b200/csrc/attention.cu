@@ -575,6 +575,7 @@ __global__ void __launch_bounds__(attn_threads(NQ), OCC)
   const int j0 = p.by_split.quotient(tiles.total * rank);
   const int nj = p.by_split.quotient(tiles.total * (rank + 1)) - j0;
   bool ok = true;
+  bool sees = false;  // (row warps) whether this thread's row sees any key
 
   // (registers move in the branches: code after a common point gets the
   // smaller share)
@@ -746,6 +747,7 @@ __global__ void __launch_bounds__(attn_threads(NQ), OCC)
     {
       const int qf = live ? base + p.by_frame.quotient(tok) : -1;
       mine = token_ranges(cs, p.by_ring, back(qf), qf, qf);
+      sees = mine.hi[0] > mine.lo[0] || mine.hi[1] > mine.lo[1] || mine.hi[2] > mine.lo[2];
     }
     const float c = p.scale_log2;
     float m = -INFINITY, l = 0.f;  // the maximum that p is relative to, and sum of p
@@ -907,7 +909,8 @@ __global__ void __launch_bounds__(attn_threads(NQ), OCC)
       __nv_bfloat16 *out = p.o + static_cast<long long>(seq) * p.o_seq +
                            static_cast<long long>(tok) * p.o_tok +
                            static_cast<long long>(head) * p.o_head;
-      const float inv = (l > 0.f || l != l) ? 1.f / l : 0.f;
+      // (a row that sees scores of -inf alone has the sum 0 and gives NaN)
+      const float inv = sees ? 1.f / l : 0.f;
       const uint32_t o = o_col + wg * o_cols + lanes;
       uint8_t *stage = smem + static_cast<uint32_t>(wg * CH) * kQChunk + quarter * 4096u;
 #pragma unroll 1
@@ -1041,18 +1044,20 @@ __global__ void __launch_bounds__(attn_threads(NQ), OCC)
         if (k < split) top = fmaxf(top, of[k].x);
       // A rank has nothing of the row where its sum is 0.  (A maximum of -inf
       // does not say so: maxima pass over NaN, so it is that of a rank whose
-      // scores are all NaN too; its sum is NaN then, and so is the row.)
+      // scores are all NaN too; its sum is NaN then, and so is the row.)  Where
+      // all ranks' sums are 0 the row sees nothing, or scores of -inf alone,
+      // which give NaN.
       float all = 0.f;
 #pragma unroll
       for (int k = 0; k < 8; ++k)
         if (k < split && of[k].y != 0.f)
           all += of[k].y * exp2_fast((of[k].x - top) * p.scale_log2);
       const float2 me = row_ml[wg * kRows + r];
-      float f = 0.f;
-      if (me.y != 0.f) f = exp2_fast((me.x - top) * p.scale_log2) / all;
+      const bool part_of = me.y != 0.f || (sees && all == 0.f);
+      const float f = part_of ? exp2_fast((me.x - top) * p.scale_log2) / all : 0.f;
       const uint32_t o = o_col + wg * o_cols + (static_cast<uint32_t>((warp % 4) * 32) << 16);
       const bool have = ok && nj > 0;  // (the same in every lane)
-      const bool some = have && me.y != 0.f;
+      const bool some = have && part_of;
       float *dst = part + (wg * kRows + r) * pitch;
 #pragma unroll 1
       for (int i = 0; i < cs.d; i += 32) {
