@@ -633,3 +633,20 @@ def test_scores_of_minus_infinity(name):
     assert odd > 0
     blank = Case(**dict(NAN_SCORES[name], k_frames=[0] * c.n), seed=6)
     assert (blank.run() == 0).all()
+
+
+@pytest.mark.parametrize("name", ["token", "token wide head", "prefill many", "frames 200",
+                                  "frame large", "ring", "ring frames", "prefill window"])
+def test_no_frames_at_all_gives_zeros(name):
+    """total = 0: the whole chunk lies before the sequence and sees nothing, as
+    with counts of 0 on the device."""
+    kw = dict(CASES[name], total=0)
+    c = Case(**kw)
+    assert (c.run() == 0).all()
+    assert (Case(**dict(kw, k_frames=[0] * c.n)).run() == 0).all()
+    k, v = c.caches()
+    nothing = k.clone()
+    cc3d.kv_append(torch.ones_like(k[:, :c.f]), torch.ones_like(k[:, :c.f]), k, v, frame=c.f,
+                   sinks=c.sinks, ring=c.ring, total=0)
+    cc3d.sync_status()
+    assert torch.equal(k.view(torch.int16), nothing.view(torch.int16))

@@ -1278,7 +1278,8 @@ cudaError_t launch_attention(AttnArgs a, const void *q, const Strides &sq, const
     *per_frame = 0;
     return across;
   };
-  const long long have = c.k_frames || c.ring > 0 ? c.slots : c.total;  // frames there are
+  // frames there are (an empty sequence still wants its zeros written)
+  const long long have = c.k_frames || c.ring > 0 ? c.slots : c.total > 0 ? c.total : 1;
   // A launch: two row tiles a CTA (d <= 128: a key tile is read once for both,
   // and one's softmax runs under the other's products), one, or one and two
   // CTAs an SM; keys split over 1 to 8 CTAs of a cluster.
