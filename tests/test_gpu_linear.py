@@ -214,3 +214,40 @@ def test_activation_over_its_whole_range(m, act):
             assert (got == v).all(), i
         else:
             assert (got.abs() <= 2.0 ** -55).all(), i
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("act", ACTS[1:])
+@pytest.mark.parametrize("m", [3, 700])
+def test_negative_tails_keep_their_relative_error(m, act, fp8):
+    """The activations' values left of zero, down to bf16's least numbers.
+
+    With 2^z the exponential in the formula, z is off by at most six fp32 half
+    steps of itself (constants and products, no cancellation), so its power by
+    2^-21 |z| of itself; the hardware's exponential (twice), reciprocal and a few
+    products add 2^-20, the erf form's fit 2^-20, the rounding 2^-8.  Absolutely,
+    half a step of bf16's least numbers (2^-134), and for the erf form, whose
+    exponential is flushed below 2^-126, that times |a| h (< 1 there)."""
+    n, k = 8192, 64
+    x = torch.zeros(m, k, device="cuda", dtype=torch.bfloat16)
+    w = torch.zeros(n, k, device="cuda", dtype=torch.bfloat16)
+    a = -torch.cat([torch.linspace(0, 130, n - 64, dtype=torch.float64),
+                    torch.logspace(2, 38, 64, dtype=torch.float64)])
+    bias = a[torch.randperm(n, generator=torch.Generator().manual_seed(1))].float().cuda()
+    scales = {}
+    if fp8:
+        x, w = x.to(torch.float8_e4m3fn), w.to(torch.float8_e4m3fn)
+        scales = dict(x_scale=1.0, w_scales=torch.ones(n, device="cuda"))
+    y = torch.empty(m, n, device="cuda", dtype=torch.bfloat16)
+    cc3d.linear(x, w, y, bias=bias, act=act, **scales)
+    cc3d.sync_status()
+    ref, _ = reference(x[:1].float(), w.float(), bias, None, act)
+    a = bias.double()
+    z = {cc3d.ACT_SILU: a, cc3d.ACT_GELU: a * a / 2, cc3d.ACT_GELU_TANH:
+         2 * math.sqrt(2 / math.pi) * (a + 0.044715 * a ** 3)}[act].abs() / math.log(2)
+    ref = torch.where(z > 1000, torch.zeros_like(ref), ref)  # (also where 64 bits overflow)
+    least = 2.0 ** -126 if act == cc3d.ACT_GELU else 2.0 ** -133
+    tol = ref.abs() * (2.0 ** -8 + 2.0 ** -19 + 2.0 ** -21 * z.clamp_max(1000)) + least
+    bad = ~((y.double() - ref).abs() <= tol)
+    assert not bad.any(), (int(bad.sum()), bias[bad[0].nonzero()[:3].flatten()].tolist(),
+                           y[bad][:3].tolist(), ref.expand_as(y)[bad][:3].tolist())

@@ -61,29 +61,37 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // cycles a warp each, relative error about 2^-21), so one reciprocal serves
 // both of a pair: 1 / d0 = d1 / (d0 d1).
 //
-//  * SiLU: a / (1 + 2^z), z = -a log2(e).
-//  * GELU, tanh form: a (1 + tanh u) / 2 = a / (1 + exp(-2 u)), z = -2 u
-//    log2(e), u = sqrt(2 / pi) (a + 0.044715 a^3).
-//    z up to 62 keeps the product of a pair finite; |y| < 2^-55 |a| beyond it.
-//    From below a counts as -128, so that -inf gives its limit, 0.
+//  * SiLU: a / (1 + exp(-a)); GELU, tanh form: a (1 + tanh u) / 2 = a / (1 +
+//    exp(-2 u)), u = sqrt(2 / pi) (a + 0.044715 a^3).  Both are max(a, 0) - |a|
+//    e / (1 + e) with e = exp(-|a|) or exp(-2 |u|), taken as the square of h =
+//    2^(log2(e) / 2): nothing overflows, and the values left of zero keep their
+//    relative error down to bf16's least numbers, which h as a normal number
+//    reaches.  |a| counts as 128 or 16 at most (e is 0 there, and +-inf give
+//    their limits).
 //  * GELU, erf form: max(a, 0) - |a| h, h = erfc(x) / 2, x = |a| / sqrt(2), as
 //    h = t P(t) exp(-x^2) with t = 1 / (1 + x / 2).  P, of degree 8, is fitted
 //    to erfcx(x) / 2t for t in (0, 1]: relative error 6e-7 in fp32.  |a| counts
 //    as 64 at most (h is 0 there, and +-inf give their limits).
 // NaN stays NaN and leaves the pair's other value alone.
-// a / (1 + 2^z)
-__device__ __forceinline__ uint64_t over_one_plus_exp2(uint64_t a, uint64_t z) {
-  const float2 e = unpair(z), f = unpair(a);
-  const float2 d = unpair(pair_add(
-      pair_of(ex2_approx(fminf(e.x, 62.f)), ex2_approx(fminf(e.y, 62.f))), pair_of(1.f, 1.f)));
-  const float r = rcp_approx(d.x * d.y);
-  return pair_mul(pair_of(max_nan(f.x, -128.f), max_nan(f.y, -128.f)),
-                  pair_mul(pair_of(r, r), pair_of(d.y, d.x)));
-}
 __device__ __forceinline__ uint64_t same(float x) { return pair_of(x, x); }
+// min(|a|, most)
+__device__ __forceinline__ uint64_t size_of(uint64_t a, float most) {
+  const float2 f = unpair(a);
+  return pair_of(fminf(fabsf(f.x), most), fminf(fabsf(f.y), most));
+}
+// max(a, 0) - x e / (1 + e), x = |a|, e = 2^(2 w)
+__device__ __forceinline__ uint64_t less_share(uint64_t a, uint64_t x, uint64_t w) {
+  const float2 f = unpair(a), g = unpair(w);
+  const uint64_t h = pair_of(ex2_approx(g.x), ex2_approx(g.y));
+  const uint64_t e = pair_mul(h, h);
+  const float2 d = unpair(pair_add(e, same(1.f)));
+  const float r = rcp_approx(d.x * d.y);
+  return pair_fma(pair_mul(x, e), pair_mul(same(-r), pair_of(d.y, d.x)),
+                  pair_of(max_nan(f.x, 0.f), max_nan(f.y, 0.f)));
+}
 __device__ __forceinline__ uint64_t gelu_erf(uint64_t a) {
   const float2 f = unpair(a);
-  const uint64_t x = pair_of(fminf(fabsf(f.x), 64.f), fminf(fabsf(f.y), 64.f));  // |a|
+  const uint64_t x = size_of(a, 64.f);
   const float2 d = unpair(pair_fma(x, same(0.35355339f), same(1.f)));
   const float2 z = unpair(pair_mul(pair_mul(x, x), same(-0.72134752f)));
   const float r = rcp_approx(d.x * d.y);
@@ -105,15 +113,18 @@ __device__ __forceinline__ void activate(uint64_t (&v)[N], int act) {
   if (act == CC3D_ACT_NONE) return;
   if (act == CC3D_ACT_SILU) {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      v[i] = over_one_plus_exp2(v[i], pair_mul(v[i], same(-1.4426950408889634f)));
+    for (int i = 0; i < N; ++i) {
+      const uint64_t x = size_of(v[i], 128.f);
+      v[i] = less_share(v[i], x, pair_mul(x, same(-0.5f * 1.4426950408889634f)));
+    }
   } else if (act == CC3D_ACT_GELU_TANH) {
-    constexpr float k0 = -2.0f * 0.79788456080286536f * 1.4426950408889634f;
+    constexpr float k0 = -0.79788456080286536f * 1.4426950408889634f;
     constexpr float k1 = 0.044715f * k0;
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      v[i] = over_one_plus_exp2(
-          v[i], pair_mul(v[i], pair_fma(pair_mul(v[i], v[i]), same(k1), same(k0))));
+    for (int i = 0; i < N; ++i) {
+      const uint64_t x = size_of(v[i], 16.f);
+      v[i] = less_share(v[i], x, pair_mul(x, pair_fma(pair_mul(x, x), same(k1), same(k0))));
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = gelu_erf(v[i]);
