@@ -577,11 +577,8 @@ __global__ void __launch_bounds__(attn_threads(NQ), OCC)
   bool ok = true;
   bool sees = false;  // (row warps) whether this thread's row sees any key
 
-  // (registers move in the branches: code after a common point gets the
-  // smaller share)
-  if (warp == 0) {
-    // ------------------------------ loads ---------------------------------------
-    if constexpr (NQ == 2) regs_fewer<kRegsFew>();
+  // ------------------------------ loads ---------------------------------------
+  auto load_role = [&]() {
     if (nj > 0 && elect_one()) {
       griddep_wait();
       const int rows = p.tok_tile * p.group;
@@ -621,9 +618,9 @@ __global__ void __launch_bounds__(attn_threads(NQ), OCC)
       for (int i = 0; i < stages; ++i)
         if (used >> i & 1u) mbar_wait_bounded(&full[i], par >> i & 1u, kDrainNs, nullptr, 0);
     }
-  } else if (warp <= 2) {
-    // ------------------------------ products ------------------------------------
-    if constexpr (NQ == 2) regs_fewer<kRegsFew>();
+  };
+  // ------------------------------ products ------------------------------------
+  auto product_role = [&]() {
     if (nj > 0 && elect_one()) {
       griddep_wait();  // (a wait's limit does not count the kernels before)
       constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, KT);
@@ -731,9 +728,9 @@ __global__ void __launch_bounds__(attn_threads(NQ), OCC)
       umma_commit(&drain[warp - 1]);
       mbar_wait_bounded(&drain[warp - 1], 0, kDrainNs, nullptr, 0);
     }
-  } else if (warp >= kFirstRowWarp) {
-    // ------------------------------ softmax, output ------------------------------
-    if constexpr (NQ == 2) regs_more<kRegsMany>();
+  };
+  // ------------------------------ softmax, output ------------------------------
+  auto row_role = [&]() {
     griddep_wait();
     const int wg = (warp - kFirstRowWarp) / 4;  // this warp's row tile
     const int quarter = warp % 4;               // the tensor-memory lanes it may read
@@ -951,8 +948,9 @@ __global__ void __launch_bounds__(attn_threads(NQ), OCC)
       }
     }
     if (split > 1) row_ml[wg * kRows + r] = make_float2(m, l);
-  } else {
-    // ------------------------------ values behind a mask --------------------------
+  };
+  // ------------------------------ values behind a mask --------------------------
+  auto mask_role = [&]() {
     // A weight of 0 times an infinity or a NaN would reach the sums.  So in the
     // tiles that a mask cuts, keys' values that are not finite where only some
     // queries see them are cleared before the products read them, and the rows
@@ -960,7 +958,6 @@ __global__ void __launch_bounds__(attn_threads(NQ), OCC)
     // may be anything: a slot never written, a frame beyond the end) are
     // cleared by the row warps once this warp says that they have landed: it
     // passes every group of the ring, so that no barrier runs ahead of it.
-    if constexpr (NQ == 2) regs_fewer<kRegsFew>();
     griddep_wait();
     constexpr int kMine = KT / 32;  // keys of a lane: lane, lane + 32, ...
     int s = 0;
@@ -1020,6 +1017,27 @@ __global__ void __launch_bounds__(attn_threads(NQ), OCC)
       ++n_masked;
       pass(NG);
     }
+  };
+  // Registers move between the warpgroups in their branches (code after a common
+  // point gets the smaller share); all warps of one execute the same instruction.
+  if constexpr (NQ == 2) {
+    if (warp >= kFirstRowWarp) {
+      regs_more<kRegsMany>();
+      row_role();
+    } else {
+      regs_fewer<kRegsFew>();
+      if (warp == 0) load_role();
+      else if (warp <= 2) product_role();
+      else mask_role();
+    }
+  } else if (warp == 0) {
+    load_role();
+  } else if (warp <= 2) {
+    product_role();
+  } else if (warp >= kFirstRowWarp) {
+    row_role();
+  } else {
+    mask_role();
   }
   if (split > 1) {
     __syncwarp();
