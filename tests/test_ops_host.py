@@ -269,3 +269,9 @@ def test_overlapping_caches_refused(lib, kw):
     before = cc3d.cc3d_launch_count()
     assert append(lib, **kw) == cc3d.ERR_ALIAS
     assert cc3d.cc3d_launch_count() == before
+
+
+@pytest.mark.parametrize("x_scale", [-1.0, float("nan"), float("inf"), 1e-38])
+def test_linear_refuses_a_second_scale_of_any_value(lib, x_scale):
+    """With one scale per row the single scale is 0, as the header says."""
+    assert linear(lib, **dict(E4M3, x_scales=0x6000000, x_scale=x_scale)) == cc3d.ERR_INVALID_ARG

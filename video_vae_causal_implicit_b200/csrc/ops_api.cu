@@ -208,8 +208,9 @@ cc3d_status cc3d_linear(const cc3d_linear_call *p, void *stream) {
     return CC3D_ERR_INVALID_ARG;
   if (dtype != CC3D_BF16 && dtype != CC3D_FP8_E4M3) return CC3D_ERR_UNSUPPORTED;
   const bool fp8 = dtype == CC3D_FP8_E4M3;
+  // (the scale that is not in use has to be 0, not only of no use)
   const bool one_scale = x_scale > 0.f && std::isfinite(x_scale);
-  if (fp8 ? (!w_scales || (x_scales != nullptr) == one_scale)
+  if (fp8 ? (!w_scales || (x_scales ? x_scale != 0.f : !one_scale))
           : (w_scales || x_scales || x_scale != 0.f))
     return CC3D_ERR_INVALID_ARG;
   const int step = fp8 ? 16 : 8;  // operand elements of 16 bytes
