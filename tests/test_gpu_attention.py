@@ -650,3 +650,30 @@ def test_no_frames_at_all_gives_zeros(name):
                    sinks=c.sinks, ring=c.ring, total=0)
     cc3d.sync_status()
     assert torch.equal(k.view(torch.int16), nothing.view(torch.int16))
+
+
+@pytest.mark.parametrize("name", ["ring", "frames", "ragged", "into sinks"])
+@pytest.mark.parametrize("level", ["heads", "tokens", "sequences"])
+def test_append_and_attention_over_interleaved_caches(name, level):
+    """Both caches as slices of one tensor: an entry's keys beside its values,
+    token by token, or sequence by sequence."""
+    c = Case(**dict(APPEND[name]), fill=3.0)
+    want_k, want_v = c.caches()
+    c.all = [a - q for a, q in zip(c.all, c.chunk)]
+    old_k, old_v = c.caches()
+    c.all = [a + q for a, q in zip(c.all, c.chunk)]
+    n, tok, kv, d = old_k.shape
+    at = {"heads": 3, "tokens": 2, "sequences": 1}[level]
+    both = torch.stack([old_k, old_v], at)
+    k, v = both.unbind(at)
+    assert not k.is_contiguous() or level == "sequences" and n == 1
+    new = torch.zeros(2, n, c.t * c.f, kv, d, device="cuda", dtype=torch.bfloat16)
+    for b in range(n):
+        a, q = c.all[b] * c.f, c.chunk[b] * c.f
+        new[0, b, :q], new[1, b, :q] = c.lk[b, a - q:a], c.lv[b, a - q:a]
+    args = c.args()
+    args.pop("window")
+    cc3d.kv_append(new[0], new[1], k, v, **args)
+    cc3d.sync_status()
+    assert torch.equal(k, want_k) and torch.equal(v, want_v)
+    c.check(c.run(k=k, v=v))
