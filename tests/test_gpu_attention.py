@@ -677,3 +677,51 @@ def test_append_and_attention_over_interleaved_caches(name, level):
     cc3d.sync_status()
     assert torch.equal(k, want_k) and torch.equal(v, want_v)
     c.check(c.run(k=k, v=v))
+
+
+# Cases for each of the kernels, with its keys in one CTA and split over a
+# cluster: (kernel, CTAs, the case).  tests/test_ops_choice.py checks on the CPU
+# that they do take them.
+_PADDED = dict(n=2, t=300, heads=32, kv=16, window=500, sinks=4, ring=800, k_frames=[2000, 900],
+               q_frames=[300, 250])
+_LONG = dict(t=300, total=4300, heads=16, kv=2, window=4000, sinks=1)
+_FRAMES = dict(n=2, frame=500, t=5, total=5, heads=2, kv=1, window=3)
+_SMALL = dict(frame=50, t=3, total=9, window=4, sinks=3)
+_TOKENS = dict(t=1111, total=2500, heads=32, kv=8, window=700, sinks=5)
+KERNELS = {
+    "two row tiles, 64": (0, 1, dict(_TOKENS, d=64)),
+    "two row tiles, 56, split": (0, 6, dict(_LONG, d=56)),
+    "two row tiles, 64, frames split": (0, 3, dict(_FRAMES, d=64)),
+    "two row tiles, 128": (1, 1, dict(_TOKENS, d=128)),
+    "two row tiles, 120, split": (1, 2, dict(n=4, t=40, total=4040, d=120, heads=48, kv=12, sinks=3)),
+    "two row tiles, 128, frames split": (1, 3, dict(_FRAMES, d=128)),
+    "two CTAs, 64": (2, 1, dict(_PADDED, d=64)),
+    "two CTAs, 64, split": (2, 8, dict(_SMALL, d=64)),
+    "two CTAs, 128": (3, 1, dict(_PADDED, d=128)),
+    "two CTAs, 120, split": (3, 8, dict(_SMALL, d=120)),
+    "128 keys, 64": (4, 1, dict(t=130, total=700, d=64, heads=32, kv=32, window=100, sinks=3)),
+    "128 keys, 64, split": (4, 4, dict(t=300, total=2300, d=64, heads=8, kv=8, window=300, sinks=2)),
+    "128 keys, 128": (5, 1, dict(t=130, total=700, d=128, heads=32, kv=32, window=100, sinks=3)),
+    "128 keys, 128, split": (5, 3, dict(_LONG, d=128)),
+    "200 channels": (6, 1, dict(t=300, total=700, d=200, heads=24, kv=24, window=100, sinks=2)),
+    "136 channels, split": (6, 3, dict(_LONG, d=136)),
+    "384 channels": (7, 1, dict(t=300, total=700, d=384, heads=24, kv=24, window=100, sinks=2)),
+    "264 channels, split": (7, 2, dict(frame=200, t=2, total=5, d=264, heads=12, kv=12, window=3,
+                                       sinks=3)),
+}
+
+
+@pytest.mark.parametrize("name", KERNELS)
+def test_every_kernel_and_split(name, monkeypatch):
+    kw = KERNELS[name][2]
+    c = Case(**kw, seed=len(name))
+    first = c.run()
+    c.check(first)
+    assert torch.equal(c.run(), first)
+    for cases in (MASKS, HIDDEN, NAN_SCORES):
+        monkeypatch.setitem(cases, name, kw)
+    test_values_that_are_not_finite_reach_the_queries_that_see_them_alone(name)
+    test_nan_queries_and_runs_of_nan_keys_are_as_in_the_definition(name)
+    if "k_frames" not in kw:  # (these two take sequences of one length)
+        test_masks_key_by_key(name)
+        test_scores_of_minus_infinity(name)

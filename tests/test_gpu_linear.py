@@ -251,3 +251,26 @@ def test_negative_tails_keep_their_relative_error(m, act, fp8):
     bad = ~((y.double() - ref).abs() <= tol)
     assert not bad.any(), (int(bad.sum()), bias[bad[0].nonzero()[:3].flatten()].tolist(),
                            y[bad][:3].tolist(), ref.expand_as(y)[bad][:3].tolist())
+
+
+# Sizes for each of the tiles and splits; tests/test_ops_choice.py checks on the
+# CPU that they do take them all.
+CHOICES = [
+    (700, 520, 96), (1000, 12288, 64), (4000, 2056, 512), (7800, 264, 1024), (7800, 264, 2048),
+    (2500, 1032, 4096), (1, 8, 64), (1, 8192, 384), (5, 4104, 1008), (2, 264, 2064), (17, 2056, 2048),
+    (33, 4096, 384), (33, 1000, 2000), (60, 2056, 512), (200, 1160, 512), (65, 2048, 528),
+    (80, 264, 2064), (90, 264, 1040), (100, 2048, 2048), (112, 136, 4096), (200, 2048, 4096),
+    (300, 1000, 4096), (512, 264, 8192), (128, 12288, 144), (100, 8, 64)]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("m,n,k", CHOICES)
+def test_every_tile_and_split(m, n, k, fp8):
+    x, w, bias, xs, ws = make(m, n, k, m + n + k, fp8)
+    res = torch.randn(m, n, device="cuda").to(torch.bfloat16)
+    for residual in (res, None):
+        y = torch.full((m, n), float("nan"), device="cuda", dtype=torch.bfloat16)
+        cc3d.linear(x, w, y, bias=bias, residual=residual, act=cc3d.ACT_GELU_TANH, x_scales=xs,
+                    w_scales=ws)
+        cc3d.sync_status()
+        check(y, *reference(x, w, bias, residual, cc3d.ACT_GELU_TANH, xs, ws), (m, n, k, fp8))

@@ -1173,7 +1173,7 @@ struct Variant {
   uint32_t smem;
   double step;
 };
-constexpr int kVariants = 8;
+constexpr int kVariants = kAttnKernels;
 template <int NQ, int KT, int CH, int OCC>
 Variant variant(int d_above, double step) {
   return Variant{attn_kernel<NQ, KT, CH, OCC>, NQ, KT, OCC, d_above, 64 * CH,
@@ -1267,24 +1267,18 @@ bool encode_heads(CUtensorMap *m, const void *base, int d, int heads, long long 
 
 }  // namespace
 
-cudaError_t launch_attention(AttnArgs a, const void *q, const Strides &sq, const void *k,
-                             const Strides &sk, const void *v, const Strides &sv, int sm_count,
-                             cudaStream_t stream) {
-  const Prepared *prepared = nullptr;
-  cudaError_t e = prepare_kernels(sm_count, &prepared);
-  if (e != cudaSuccess) return e;
-  const CacheShape &c = a.c;
-  a.group = a.heads / c.kv_heads;
-  a.tok_tile = kRows / a.group;
+int choose_attention(const CacheShape &c, int heads, int window, int sm_count,
+                     const int (*fits)[9], AttnLaunch *out) {
+  const long long tok_tile = kRows / (heads / c.kv_heads);
   const long long tokens = static_cast<long long>(c.t) * c.frame;
-  const long long heads = static_cast<long long>(c.n) * c.kv_heads;
+  const long long groups = static_cast<long long>(c.n) * c.kv_heads;
   // frames that a query sees
-  const long long seen = a.window > 0 ? static_cast<long long>(a.window) + c.sinks : c.slots;
+  const long long seen = window > 0 ? static_cast<long long>(window) + c.sinks : c.slots;
   // Row tiles of a CTA, its query tokens, and the tiles of a chunk.  Tiles
   // that cross frames see the keys of all of their frames; tiles that end
   // with their frame leave rows unused: whichever reads fewer keys.
   auto tile_count = [&](int nq, int *per_frame) {
-    const long long rows = static_cast<long long>(nq) * a.tok_tile;
+    const long long rows = static_cast<long long>(nq) * tok_tile;
     const long long across = (tokens + rows - 1) / rows;
     const long long within = (c.frame + rows - 1) / rows;
     const double cost_across = static_cast<double>(across) * (seen + (rows - 1.0) / c.frame);
@@ -1311,7 +1305,7 @@ cudaError_t launch_attention(AttnArgs a, const void *q, const Strides &sq, const
   // frames add)
   auto key_tiles = [&](const Variant &v, int per_frame) {
     const long long span =
-        per_frame > 0 ? 1 : (static_cast<long long>(v.nq) * a.tok_tile - 1) / c.frame + 1;
+        per_frame > 0 ? 1 : (static_cast<long long>(v.nq) * tok_tile - 1) / c.frame + 1;
     const long long frames = seen + (span < c.t ? span : c.t) - 1;
     const long long keys = (frames < have ? frames : have) * c.frame;
     return static_cast<double>((keys + v.kt - 1) / v.kt);
@@ -1329,21 +1323,21 @@ cudaError_t launch_attention(AttnArgs a, const void *q, const Strides &sq, const
     Launch best = {nullptr, 1, 0, 0, 1e300};
     for (const Variant &v : variants()) {
       if (c.d > v.d_most || c.d <= v.d_above) continue;
-      const long long rows = static_cast<long long>(v.nq) * a.tok_tile;
+      const long long rows = static_cast<long long>(v.nq) * tok_tile;
       if (skip % rows != 0) continue;
       int per_frame = 0;
       const long long tiles = tile_count(v.nq, &per_frame) - skip / rows;
-      if (tiles * heads > INT32_MAX / 8) continue;
+      if (tiles * groups > INT32_MAX / 8) continue;
       const double steps = key_tiles(v, per_frame);
       for (int split = 1; split <= 8 && split <= steps; ++split) {
-        const int fit = prepared->fit[&v - variants()][split];
+        const int fit = fits[&v - variants()][split];
         if (fit < 1) continue;
         // (a few waves are whole ones; the last of many overlaps the others')
-        const double parts = static_cast<double>(tiles * heads) / fit;
+        const double parts = static_cast<double>(tiles * groups) / fit;
         const double waves = parts < 4.0 ? std::ceil(parts) : parts + 0.5;
         // (alone on its SM a CTA of a pair steps faster)
         const double step =
-            v.occ == 2 && tiles * heads * split <= sm_count ? 0.85 * v.step : v.step;
+            v.occ == 2 && tiles * groups * split <= sm_count ? 0.85 * v.step : v.step;
         const double t = time_of(v, steps, split, waves, step);
         if (t < best.time) best = {&v, split, per_frame, tiles, t};
       }
@@ -1351,7 +1345,7 @@ cudaError_t launch_attention(AttnArgs a, const void *q, const Strides &sq, const
     return best;
   };
   Launch parts[2] = {fastest(0), {}};
-  if (!parts[0].kernel) return cudaErrorNotSupported;  // (too many tiles for a grid)
+  if (!parts[0].kernel) return 0;
   int n_parts = 1;
   // The queries of one frame, of which all see the same keys, may also go in
   // two launches: whole waves of full tiles, and what is left with more CTAs a
@@ -1366,14 +1360,14 @@ cudaError_t launch_attention(AttnArgs a, const void *q, const Strides &sq, const
     double least = 0.97 * parts[0].time - 4000.0;
     for (const Variant &v : variants()) {
       if (c.d > v.d_most || c.d <= v.d_above) continue;
-      const long long rows = static_cast<long long>(v.nq) * a.tok_tile;
+      const long long rows = static_cast<long long>(v.nq) * tok_tile;
       const double steps = key_tiles(v, 0);
       for (int split = 1; split <= 8 && split <= steps; ++split) {
-        const int fit = prepared->fit[&v - variants()][split];
+        const int fit = fits[&v - variants()][split];
         for (int waves = 1; waves <= 3; ++waves) {
-          long long tiles = static_cast<long long>(waves) * fit / heads;
+          long long tiles = static_cast<long long>(waves) * fit / groups;
           if (tiles > tokens / rows) tiles = tokens / rows;
-          if (tiles < 1 || tiles * rows >= tokens || tiles * heads > INT32_MAX / 8) continue;
+          if (tiles < 1 || tiles * rows >= tokens || tiles * groups > INT32_MAX / 8) continue;
           const double first = time_of(v, steps, split, waves, v.step);
           if (first >= least) break;
           const Launch rest = fastest(tiles * rows);
@@ -1387,6 +1381,26 @@ cudaError_t launch_attention(AttnArgs a, const void *q, const Strides &sq, const
       }
     }
   }
+  for (int i = 0; i < n_parts; ++i)
+    out[i] = AttnLaunch{static_cast<int>(parts[i].kernel - variants()), parts[i].split,
+                        parts[i].per_frame, parts[i].tiles};
+  return n_parts;
+}
+
+cudaError_t launch_attention(AttnArgs a, const void *q, const Strides &sq, const void *k,
+                             const Strides &sk, const void *v, const Strides &sv, int sm_count,
+                             cudaStream_t stream) {
+  const Prepared *prepared = nullptr;
+  cudaError_t e = prepare_kernels(sm_count, &prepared);
+  if (e != cudaSuccess) return e;
+  const CacheShape &c = a.c;
+  a.group = a.heads / c.kv_heads;
+  a.tok_tile = kRows / a.group;
+  const long long tokens = static_cast<long long>(c.t) * c.frame;
+  const long long groups = static_cast<long long>(c.n) * c.kv_heads;
+  AttnLaunch parts[2];
+  const int n_parts = choose_attention(c, a.heads, a.window, sm_count, prepared->fit, parts);
+  if (n_parts == 0) return cudaErrorNotSupported;  // (too many tiles for a grid)
   a.by_frame = FastDiv(static_cast<uint32_t>(c.frame));
   a.by_group = FastDiv(static_cast<uint32_t>(a.group));
   a.by_kv = FastDiv(static_cast<uint32_t>(c.kv_heads));
@@ -1398,7 +1412,7 @@ cudaError_t launch_attention(AttnArgs a, const void *q, const Strides &sq, const
     return cudaErrorInvalidValue;
   long long first_row = 0;  // query tokens of the launch before
   for (int i = 0; i < n_parts; ++i) {
-    const Variant &v0 = *parts[i].kernel;
+    const Variant &v0 = variants()[parts[i].kernel];
     const long long rows = static_cast<long long>(v0.nq) * a.tok_tile;
     a.q_tiles = static_cast<int>(parts[i].tiles);
     a.tile0 = static_cast<int>(first_row / rows);
@@ -1407,7 +1421,7 @@ cudaError_t launch_attention(AttnArgs a, const void *q, const Strides &sq, const
     a.tiles_frame = parts[i].per_frame;
     a.by_split = FastDiv(static_cast<uint32_t>(a.split));
     a.by_tiles_frame = FastDiv(static_cast<uint32_t>(a.tiles_frame > 0 ? a.tiles_frame : 1));
-    const long long grid = parts[i].tiles * heads * a.split;
+    const long long grid = parts[i].tiles * groups * a.split;
     if (grid > INT32_MAX) return cudaErrorNotSupported;
     CUtensorMap mk, mv;
     if (!encode_heads(&mk, k, c.d, c.kv_heads, cached, c.n, sk, 1, v0.kt) ||

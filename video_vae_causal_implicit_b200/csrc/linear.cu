@@ -705,11 +705,6 @@ const LinearKernel kLinear[2][2] = {{linear_kernel<false, false>, linear_kernel<
                                     {linear_kernel<true, false>, linear_kernel<true, true>}};
 const SplitKernel kSplit[2] = {linear_split_kernel<false>, linear_split_kernel<true>};
 
-struct Choice {
-  bool split_kernel;
-  int pair, nt, stages, split;
-};
-
 int many_stages(int pair, int nt) {
   int st = 8;
   while (ring_layout(pair ? nt / 2 : nt, st, nt).total + 1024 > kSmemMost) --st;
@@ -797,41 +792,44 @@ cudaError_t prepare_kernels(int sm_count, const Prepared **out) {
   return cudaSuccess;
 }
 
+}  // namespace
+
 // Estimated cycles, from measurements of both kernels at K = 384 to 8192 and 1
 // to 16384 rows.  Many rows: rounds of tiles, each the longest of its products
 // (four a chunk, N / 2 + 44 cycles), its operands (68 bytes a cycle and SM from
 // L2) and its epilogue.  Few rows: the operands' bytes at 45 a cycle and SM and
 // at 3500 from HBM, and the joining of the parts.
-Choice choose(const LinearArgs &a, bool fp8, int sm_count, const Prepared &pre) {
-  const int nk = (a.k + (fp8 ? 127 : 63)) / (fp8 ? 128 : 64);
-  Choice best = {};
+LinearChoice choose_linear(int m, int n, int k, int act, bool fp8, int sm_count, int pairs,
+                           const int (*clusters)[9]) {
+  const int nk = (k + (fp8 ? 127 : 63)) / (fp8 ? 128 : 64);
+  LinearChoice best = {};
   double best_t = 1e300;
   const int shapes[4][2] = {{1, 256}, {1, 128}, {0, 128}, {0, 64}};
   for (const auto &sh : shapes) {
     const int pair = sh[0], nt = sh[1], rows = pair ? 256 : 128;
-    const double tiles = static_cast<double>((a.m + rows - 1) / rows) * ((a.n + nt - 1) / nt);
-    const int slots = pair ? pre.pairs[fp8] : sm_count;
+    const double tiles = static_cast<double>((m + rows - 1) / rows) * ((n + nt - 1) / nt);
+    const int slots = pair ? pairs : sm_count;
     const double rounds = std::ceil(tiles / slots);
     const double bytes = kAStage + (pair ? nt / 2 : nt) * static_cast<double>(kRowBytes);
-    const double epi = 600.0 + nt * (a.act == CC3D_ACT_NONE ? 14.0 : 30.0);
+    const double epi = 600.0 + nt * (act == CC3D_ACT_NONE ? 14.0 : 30.0);
     double per = nk * 4.0 * (nt / 2.0 + 44.0);
     per = std::fmax(per, nk * bytes / 68.0);
     per = std::fmax(per, epi);
     const double t = 5500.0 + 1000.0 * pair + epi + rounds * (per + 500.0);
     if (t < best_t) {
       best_t = t;
-      best = Choice{false, pair, nt, many_stages(pair, nt), 1};
+      best = LinearChoice{false, pair, nt, many_stages(pair, nt), 1};
     }
   }
-  if (a.m <= 512) {
+  if (m <= 512) {
     int nt = 16;
-    while (nt < a.m && nt < 128) nt += 16;
-    for (; nt >= 64 || nt >= a.m; nt -= 64) {  // (the tokens' own tile, and a half of 128)
-      const double tiles = static_cast<double>((a.n + 127) / 128) * ((a.m + nt - 1) / nt);
-      const double hbm = (static_cast<double>(a.n) + a.m) * nk * kRowBytes / 3500.0;
+    while (nt < m && nt < 128) nt += 16;
+    for (; nt >= 64 || nt >= m; nt -= 64) {  // (the tokens' own tile, and a half of 128)
+      const double tiles = static_cast<double>((n + 127) / 128) * ((m + nt - 1) / nt);
+      const double hbm = (static_cast<double>(n) + m) * nk * kRowBytes / 3500.0;
       const double bytes = kAStage + nt * static_cast<double>(kRowBytes);
       for (int split = 1; split <= 8 && split <= nk; ++split) {
-        const int fit = pre.clusters[fp8][nt / 16][split];
+        const int fit = clusters[nt / 16][split];
         if (fit < 1) continue;
         const double waves = std::ceil(tiles / fit);
         const double share = tiles * split > sm_count ? 1.8 : 1.0;  // two CTAs of an SM
@@ -840,7 +838,7 @@ Choice choose(const LinearArgs &a, bool fp8, int sm_count, const Prepared &pre) 
                          std::hypot(hbm, stream) + 900.0 * (waves - 1.0);
         if (t < best_t) {
           best_t = t;
-          best = Choice{true, 0, nt, split_stages(nt), split};
+          best = LinearChoice{true, 0, nt, split_stages(nt), split};
         }
       }
       if (nt <= 64) break;
@@ -849,14 +847,13 @@ Choice choose(const LinearArgs &a, bool fp8, int sm_count, const Prepared &pre) 
   return best;
 }
 
-}  // namespace
-
 cudaError_t launch_linear(LinearArgs a, const void *x, long long ldx, const void *w,
                           long long ldw, bool fp8, int sm_count, cudaStream_t stream) {
   const Prepared *pre = nullptr;
   cudaError_t e = prepare_kernels(sm_count, &pre);
   if (e != cudaSuccess) return e;
-  const Choice c = choose(a, fp8, sm_count, *pre);
+  const LinearChoice c = choose_linear(a.m, a.n, a.k, a.act, fp8, sm_count, pre->pairs[fp8],
+                                       pre->clusters[fp8]);
   a.nt = c.nt;
   a.stages = c.stages;
   a.split = c.split;

@@ -92,6 +92,17 @@ struct LinearArgs {
 cudaError_t launch_linear(LinearArgs a, const void *x, long long ldx, const void *w,
                           long long ldw, bool fp8, int sm_count, cudaStream_t stream);
 
+// What a call launches: the many-row kernel with tiles of nt columns (on CTA
+// pairs or not), or the few-row kernel with nt tokens and K split over `split`
+// CTAs.  pairs: CTA pairs of the former, clusters[nt / 16][split]: clusters of
+// the latter that are resident at once.
+struct LinearChoice {
+  bool split_kernel;
+  int pair, nt, stages, split;
+};
+LinearChoice choose_linear(int m, int n, int k, int act, bool fp8, int sm_count, int pairs,
+                           const int (*clusters)[9]);
+
 // Which frame of a sequence a cache slot holds: slot s < sinks frame s; the
 // later slots frame s (ring 0), or cyclically the last `ring` frames.
 struct CacheShape {
@@ -122,6 +133,18 @@ struct Strides {
 cudaError_t launch_attention(AttnArgs a, const void *q, const Strides &sq, const void *k,
                              const Strides &sk, const void *v, const Strides &sv, int sm_count,
                              cudaStream_t stream);
+// What a call launches: the kernel (by its place in the list of them), the CTAs
+// that share a query tile's keys, query tiles of a frame (0: tiles cross
+// frames) and of the launch.  Returns the number of launches (1 or 2; 0: too
+// many tiles for a grid).  fits[kernel][split]: clusters of that many CTAs that
+// are resident at once.
+constexpr int kAttnKernels = 8;
+struct AttnLaunch {
+  int kernel, split, per_frame;
+  long long tiles;
+};
+int choose_attention(const CacheShape &c, int heads, int window, int sm_count,
+                     const int (*fits)[9], AttnLaunch *out);
 cudaError_t launch_kv_append(const CacheShape &c, const __nv_bfloat16 *k, const Strides &sk,
                              const __nv_bfloat16 *v, const Strides &sv, __nv_bfloat16 *kc,
                              const Strides &skc, __nv_bfloat16 *vc, const Strides &svc,
