@@ -73,3 +73,57 @@ def test_bounded_waits_report_timeout_and_leave_context_usable():
         # may come within the limit)
         assert first == TIMEOUT or (name.startswith("maybe") and first == OK), name
         assert second == OK, name  # reading the status clears it
+
+
+# Each step of these takes more bytes from HBM than come within a microsecond
+# (at the 6.5 TB/s of all SMs together, behind a latency of some 0.7): 148 CTAs
+# whose tile of keys has 16 KB (64 channels, 128 keys) to 48 KB, or two CTAs an SM.
+STRICT = CHILD[:CHILD.index("def status")] + r"""
+def attention(name, n, t, total, heads, kv, d, **kw):
+    q = torch.randn(n, t, heads, d, **b16)
+    k, v = torch.randn(n, total, kv, d, **b16), torch.randn(n, total, kv, d, **b16)
+    o = torch.empty_like(q)
+    seen = []
+    for _ in range(4):
+        flush.zero_()             # (the inputs have to come from HBM)
+        torch.cuda.synchronize()
+        before = cc3d.cc3d_launch_count()
+        cc3d.attention(q, k, v, o, total=total // kw.get('frame', 1), **kw)
+        assert cc3d.cc3d_launch_count() == before + 1
+        seen.append(cc3d.cc3d_sync_status(cc3d._stream()))
+    out[name] = seen
+
+flush = torch.empty(1 << 28, device='cuda', dtype=torch.float32)
+for name, kw in %r.items():
+    attention(name, **kw)
+torch.cuda.synchronize()
+out['torch_after'] = (torch.arange(1024, device='cuda', dtype=torch.float32) * 2).sum().item()
+print('RESULT ' + json.dumps(out))
+"""
+SPLITS = {
+    "one token": dict(n=16, t=1, total=20000, heads=8, kv=2, d=128),
+    "one token, 64 channels": dict(n=16, t=1, total=20000, heads=8, kv=2, d=64),
+    "one token, 256 channels": dict(n=8, t=1, total=20000, heads=8, kv=2, d=256),
+    "one token, 384 channels": dict(n=8, t=1, total=20000, heads=2, kv=2, d=384),
+    "frames": dict(n=1, t=7800, total=7800, heads=1, kv=1, d=384, frame=1560, window=1),
+    "two row tiles": dict(n=1, t=3000, total=3000, heads=2, kv=2, d=128, frame=1000),
+}
+PAIRS = {
+    "two CTAs an SM, 64 channels": dict(n=64, t=64, total=1500, heads=16, kv=16, d=64, window=300),
+    "two CTAs an SM": dict(n=64, t=64, total=1500, heads=16, kv=16, d=128, window=300),
+}
+
+
+def test_waits_of_split_keys_and_of_two_ctas_an_sm_run_out():
+    """A split's ranks meet at cluster barriers after a wait of one of them ran
+    out, too: every call returns, and some report it."""
+    env = dict(os.environ, CC3D_WAIT_LIMIT_US="1")
+    proc = subprocess.run([sys.executable, "-c", STRICT % dict(SPLITS, **PAIRS)], env=env,
+                          capture_output=True, text=True, timeout=300)
+    assert proc.returncode == 0, proc.stderr[-3000:]
+    line = [l for l in proc.stdout.splitlines() if l.startswith("RESULT ")][-1]
+    res = json.loads(line[len("RESULT "):])
+    assert res.pop("torch_after") == float(sum(range(1024)) * 2)
+    assert set(res) == set(SPLITS) | set(PAIRS)
+    for name, got in res.items():
+        assert len(got) == 4 and set(got) <= {0, 7} and 7 in got, (name, got)

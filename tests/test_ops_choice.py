@@ -13,6 +13,7 @@ import pytest
 
 from tests.test_gpu_attention import KERNELS, LONG_FRAMES
 from tests.test_gpu_linear import CHOICES
+from tests.test_gpu_ops_failure import PAIRS, SPLITS
 from video_vae_causal_implicit_b200 import build as cbuild
 from video_vae_causal_implicit_b200 import cc3d
 
@@ -64,6 +65,17 @@ def test_gpu_cases_take_the_kernels_they_are_for(probe):
         assert [x[:2] for x in launches(row)] == [(kernel, split)], name
     assert {(k, s > 1) for k, s, _ in KERNELS.values()} == {
         (k, many) for k in range(8) for many in (False, True)}
+
+
+def test_cases_whose_waits_run_out_are_splits_and_pairs_of_ctas(probe):
+    def case(t, total, frame=1, **kw):
+        return attention(t=t // frame, total=total // frame, frame=frame, **kw)
+    rows = [launches(r) for r in probe([case(**kw) for kw in (SPLITS | PAIRS).values()])]
+    got = {name: (len(r), *r[0][:2]) for name, r in zip(SPLITS | PAIRS, rows)}
+    assert all(n == 1 for n, _, _ in got.values()), got
+    assert all(got[name][2] > 1 for name in SPLITS), got
+    assert {got[name][1] for name in SPLITS} >= {1, 4, 5, 6, 7}, got
+    assert {got[name][1:] for name in PAIRS} == {(2, 1), (3, 1)}, got
 
 
 def test_long_frames_go_in_two_launches(probe):
