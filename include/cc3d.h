@@ -417,7 +417,10 @@ typedef enum {
  * zeros, at least 1e-36), or s = scale for every row.  eps = 0 gives
  * rms_norm's definition, eps > 0 the one with the mean square + eps.  The
  * codes feed cc3d_linear (scales as its x_scales) or, with one scale, a
- * CC3D_FP8_E4M3 conv plan (scale as its x_scale).
+ * CC3D_FP8_E4M3 conv plan (scale as its x_scale).  (y alone, with eps = 0 and
+ * no residual, is what rms_norm and rmsnorm_silu compute; those keep the convs'
+ * frame caches, this call takes any rows and c up to 16384.)  SiLU's values
+ * under 1e-36 in magnitude count as 0.
  *   x, residual, h, y  [rows][c] bf16, 16-byte aligned; residual, h, y
  *                      nullable; h and y may be x or the residual itself
  *   q                  [rows][c] bytes, 8-byte aligned, nullable
@@ -473,7 +476,8 @@ cc3d_status cc3d_linear(const cc3d_linear_call *call, void *stream);
  * the keys of frame j when j <= i and (window == 0 or i - j < window or
  * j < sinks):
  *   o = sum_j softmax_j(scale * q . k_j) v_j   over the keys it sees;
- * a query that sees none gives zeros.  frame = 1 is the token-wise sliding
+ * a query that sees none gives zeros (one that sees scores of -inf alone, or a
+ * NaN, gives NaN).  frame = 1 is the token-wise sliding
  * window; window = 1 with sinks = 0 is the mid-block's attention within each
  * frame ("Cosmos3 Wan VAE" §10.6, WanAttentionBlock).
  *

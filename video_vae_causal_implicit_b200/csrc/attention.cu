@@ -16,7 +16,8 @@
 // softmax carry no more than the inputs' 8 bits) and feeds the second
 // product from there.  O is rescaled only when a row's maximum has grown by
 // more than 2^8 since the last time: until then p may reach 256, which
-// changes no rounding error (bf16 and fp32 are relative).
+// changes no rounding error (bf16 and fp32 are relative).  l sums the weights
+// before their rounding.
 //
 // Keys are walked in the cache's own order, tile by tile; tiles no query of
 // the CTA sees are skipped, tiles all of them see are not masked.  With few
@@ -25,11 +26,13 @@
 //
 // Bound: the tensor pipe and the exponentials (16 a cycle and SM, as many
 // cycles as the two products take at d = 128) for many rows, the cache's
-// bytes for one token.  Measured: 8190 tokens, 16 heads on 4 of d = 128, window
-// 2048 and 4 sinks 122 us (990 TFLOP/s; a step of 64 keys takes a CTA's 256
-// rows about 1670 cycles, of which the products want 1130 and the exponentials
-// 1024); frames of 1560 tokens, d = 384, within themselves 31 us for five; one
-// token of 8 sequences, 32 heads on 8, over 8208 cached 47 us (5.7 TB/s).
+// bytes for one token.  Measured (device time, twelve calls in a graph, one of
+// several GPUs, whose clocks under load differ by 5 %): 8190 tokens, 16 heads on
+// 4 of d = 128, window 2048 and 4 sinks 129 us (930 TFLOP/s; a step of 64 keys
+// takes a CTA's 256 rows about 1670 cycles, of which the products want 1130 and
+// the exponentials 1024); frames of 1560 tokens, d = 384, within themselves 32
+// us for five; one token of 8 sequences, 32 heads on 8, over 8208 cached 47 us
+// (5.7 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -162,8 +165,8 @@ __device__ __forceinline__ void lengths(const CacheShape &c, int seq, int &chunk
 // one barrier each: whole tiles where several fit beside Q, pairs of chunks for
 // wide heads (a slot is then free, and its next load on its way, as soon as
 // the products of one pair have read it; single chunks, with twice the
-// barriers, took 38.5 us where pairs take 30.7: five frames of 1560 tokens, d =
-// 384).  P V runs in steps of PC chunks (N = 64 PC).
+// barriers, took a quarter longer: five frames of 1560 tokens, d = 384).  P V
+// runs in steps of PC chunks (N = 64 PC).
 template <int NQ, int KT, int CH, int OCC>
 struct Shape {
   static constexpr int GC = CH <= 2 ? CH : 2;
@@ -837,9 +840,10 @@ __global__ void __launch_bounds__(attn_threads(NQ), OCC)
               pair_of(__uint_as_float(raw[i + e]), __uint_as_float(raw[i + e + 1])), c2, mc2));
           // With 128 keys a tile a warp has its scheduler to itself and waits
           // for the exponential's unit: three pairs of eight take the other way
-          // (one token over a long cache 46.9 -> 45.6 us; four of eight 48.5.
-          // With two row tiles the warps' instructions bound: 124 us at 8190
-          // tokens with none or one of eight, 129 with two).
+          // (one token over a long cache 3 % faster, with four of eight 3 %
+          // slower than with none.  With two row tiles the warps' instructions
+          // bound: 8190 tokens take the same with none or one of eight, 4 % more
+          // with two).
           const bool products = KT == 128 && (0x92 >> ((e / 2) % 8) & 1);
           const float2 y =
               products ? exp2_products(x) : make_float2(exp2_fast(x.x), exp2_fast(x.y));
@@ -851,7 +855,7 @@ __global__ void __launch_bounds__(attn_threads(NQ), OCC)
         const float2 x = unpair(pair_add(sum[0], sum[1]));
         l += x.x + x.y;
       }
-      // (stores within the turn: 130.5 us where this takes 127.9, at 8190 tokens)
+      // (stores within the turn: 2 % slower at 8190 tokens)
       pass_turn(j);
 #pragma unroll
       for (int i = 0; i < KT / 2; i += 16) tmem_st16(sc + i, raw + i);

@@ -10,15 +10,17 @@
 //    CTA pair), operands by TMA through a ring of 128-byte K chunks, two
 //    accumulators in tensor memory so that a tile's epilogue runs under the
 //    next tile's MMAs.  Bound: the tensor pipe for long K (8190 x 8192 to 2048
-//    in bf16: 195 us, 1.4 PFLOP/s, at the power limit's clock), the epilogue for
-//    short K (7800 x 2048 to 8192 in FP8: 91 us without an activation, 101 with
-//    GELU's tanh form; 7800 x 384 to 1152 in bf16: 9.8 us, 2.5 TB/s).
+//    in bf16: 194 us, 1.42 PFLOP/s), the epilogue for short K (7800 x 2048 to
+//    8192 in FP8: 91 us without an activation, 101 with GELU's tanh form; 7800 x
+//    384 to 1152 in bf16: 10.1 us, 2.5 TB/s; 384 to 384 + residual 7.2).
 //  * linear_split_kernel, few rows: bound by the weights' bytes.  The roles
 //    are swapped (the 128 MMA rows are output channels, the columns are the
 //    few tokens), and a cluster of CTAs splits K so that every SM streams
 //    weights; the partial products meet in distributed shared memory, added
 //    in rank order (the result does not depend on scheduling).  One row, 2048
-//    to 12288: 11.9 us, of which the weights' 50 MB want 7.7.
+//    to 12288: 11.9 us, of which the weights' 50 MB want 7.7; in FP8 8.0 of 3.9.
+// (Device times of twelve calls in a graph.  In a long run of calls the power
+// limit's clock makes the longest ones a fifth longer: 194 us 232, 101 us 123.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
